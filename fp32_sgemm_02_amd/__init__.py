@@ -17,10 +17,11 @@ import os
 
 __all__ = [
     "sgemm", "sgemm_ex", "sgemm_op", "sgemm_op_noalloc", "sgemm_cblas", "sgemm_epilogue", "sgemm_strided_batched",
-    "sgemm_mixed", "gemm", "gemm_batched", "gemm_mixed", "select", "tile_count", "tile_info", "status_string",
+    "sgemm_mixed", "gemm", "gemm_batched", "gemm_mixed", "linear", "linear_backward", "moe",
+    "sgemm_linear", "sgemm_linear_backward", "sgemm_moe", "select", "tile_count", "tile_info", "status_string",
     "version", "workspace_release", "plan", "SgemmConfig", "TileDesc", "SgemmError", "LIB_PATH",
     "VARIANT_AUTO", "VARIANT_MFMA", "VARIANT_VALU", "VARIANT_SKINNY", "VARIANT_MFMA16",
-    "VARIANT_GENERIC16", "VARIANT_SMALL", "DTYPE_BF16", "DTYPE_F16", "FLAG_SCALAR_IO", "FLAG_UNTUNED", "FLAG_STREAMK",
+    "VARIANT_GENERIC16", "VARIANT_SMALL", "DTYPE_F32", "DTYPE_BF16", "DTYPE_F16", "FLAG_SCALAR_IO", "FLAG_UNTUNED", "FLAG_STREAMK",
     "TILE_WHOLE", "TILE_DIRECT", "TILE_TRANS_B", "TILE_TRANS_A", "TILE_STREAMK",
     "ACT_NONE", "ACT_RELU", "ACT_SILU", "ACT_GELU_ERF", "ACT_GELU_TANH",
 ]
@@ -30,7 +31,7 @@ LIB_PATH = os.path.join(_HERE, "libfp32sgemm.so")
 
 VARIANT_AUTO, VARIANT_MFMA, VARIANT_VALU, VARIANT_SKINNY = 0, 1, 2, 3
 VARIANT_MFMA16, VARIANT_GENERIC16, VARIANT_SMALL = 4, 5, 6
-DTYPE_BF16, DTYPE_F16 = 1, 2
+DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
 FLAG_SCALAR_IO = 0x1
 FLAG_UNTUNED = 0x2
 FLAG_STREAMK = 0x4
@@ -103,6 +104,12 @@ def _load():
     lib.sgemm_mixed.argtypes = [i, i, i, i, i, i, f, p, i, p, i, f, p, i, p]
     lib.sgemm_mixed_ex.restype = i
     lib.sgemm_mixed_ex.argtypes = lib.sgemm_mixed.argtypes + [ctypes.POINTER(SgemmConfig)]
+    lib.sgemm_linear.restype = i
+    lib.sgemm_linear.argtypes = [i, i, i, i, p, i, p, i, p, p, i, i, p, i, p, i, p]
+    lib.sgemm_linear_backward.restype = i
+    lib.sgemm_linear_backward.argtypes = [i, i, i, i, p, i, p, i, i, p, i, p, i, p, i, p, i, p, p]
+    lib.sgemm_moe.restype = i
+    lib.sgemm_moe.argtypes = [i, i, i, i, i, i, i, i, i, p, i, p, i, p, i, ll, p, i, ll, p, i, p, p, p]
     lib.sgemm_cblas.restype = i
     lib.sgemm_cblas.argtypes = [i, i, i, i, i, i, f, p, i, p, i, f, p, i, p]
     lib.sgemm_op_plan.restype = i
@@ -191,6 +198,27 @@ def sgemm_cblas(order, trans_a, trans_b, M, N, K, alpha, A, lda, B, ldb, beta, C
     102 column-major; trans 111 / 112 / 113)."""
     return _load().sgemm_cblas(order, trans_a, trans_b, M, N, K, alpha, A, lda, B, ldb, beta, C,
                                ldc, stream)
+
+
+def sgemm_linear(dtype, M, N, K, X, ldx, W, ldw, bias, R, ldr, act, Y, ldy, Z, ldz,
+                 stream=None) -> int:
+    """Raw C-ABI call: device addresses (int) or None; returns the status."""
+    return _load().sgemm_linear(dtype, M, N, K, X, ldx, W, ldw, bias, R, ldr, act, Y, ldy, Z, ldz,
+                                stream)
+
+
+def sgemm_linear_backward(dtype, M, N, K, dY, lddy, Z, ldz, act, X, ldx, W, ldw, dX, lddx, dW,
+                          lddw, db, stream=None) -> int:
+    """Raw C-ABI call: device addresses (int) or None; returns the status."""
+    return _load().sgemm_linear_backward(dtype, M, N, K, dY, lddy, Z, ldz, act, X, ldx, W, ldw, dX,
+                                         lddx, dW, lddw, db, stream)
+
+
+def sgemm_moe(dtype, T, D, F, E, top_k, gated, renormalize, act, X, ldx, Wr, ldr, W1, ld1, stride1,
+              W2, ld2, stride2, Y, ldy, ids=None, weights=None, stream=None) -> int:
+    """Raw C-ABI call: device addresses (int) or None; returns the status."""
+    return _load().sgemm_moe(dtype, T, D, F, E, top_k, gated, renormalize, act, X, ldx, Wr, ldr, W1,
+                             ld1, stride1, W2, ld2, stride2, Y, ldy, ids, weights, stream)
 
 
 def select(M, N, K, A=None, lda=None, B=None, ldb=None, C=None, ldc=None, *,
@@ -431,3 +459,180 @@ def gemm_batched(A, B, C=None, alpha: float = 1.0, beta: float = 0.0, *, trans_a
     if st != 0:
         raise SgemmError(st)
     return C
+
+
+# ---- the feed-forward operators ------------------------------------------------
+
+_codes = None
+
+
+def _type_code(name, t, torch) -> int:
+    global _codes
+    if _codes is None:
+        _codes = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
+    code = _codes.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    return code
+
+
+def _operand(name, t, shape, dtype, device):
+    """(address, leading dimension) of a row-major matrix of this shape, type
+    and device."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be {dtype} on {device}")
+    ld = t.stride(0)
+    if shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: rows must be contiguous (stride(1) == 1)")
+    if shape[0] <= 1 or shape[1] == 0:
+        ld = max(ld, shape[1], 1)
+    elif ld < shape[1]:
+        raise ValueError(f"{name}: rows must not overlap")
+    return t.data_ptr() or None, ld
+
+
+def _vector(name, t, n, dtype, device):
+    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous vector of {n} values")
+    if t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be {dtype} on {device}")
+    return t.data_ptr() or None
+
+
+def _result(name, t, shape, dtype, device, torch):
+    """(tensor, address, leading dimension) of a result, allocated when not given."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+        return t, t.data_ptr() or None, max(shape[1], 1)
+    return (t, *_operand(name, t, shape, dtype, device))
+
+
+def linear(X, W, bias=None, *, act: int = ACT_NONE, residual=None, keep_pre: bool = False,
+           out=None, pre=None, stream=None):
+    """act(X @ W.T + bias) + residual for 2-D float32, bfloat16 or float16 CUDA
+    tensors of one type (sgemm_linear): a linear layer with its whole epilogue,
+    computed in fp32 and rounded once.  X is M x K, W N x K, bias N values,
+    residual M x N; rows contiguous, padded rows are used through their leading
+    dimension.  keep_pre also returns X @ W.T + bias, the activation's input,
+    for linear_backward: (Y, Z).  out and pre receive Y and Z when given (out
+    may be residual itself).  Runs asynchronously on ``stream`` (default: the
+    current stream of X's device)."""
+    import torch
+
+    code = _type_code("X", X, torch)
+    if X.dim() != 2 or W.dim() != 2:
+        raise ValueError("X and W must be 2-D")
+    dtype, device = X.dtype, X.device
+    M, K = X.shape
+    N = W.shape[0]
+    x, ldx = _operand("X", X, (M, K), dtype, device)
+    w, ldw = _operand("W", W, (N, K), dtype, device)
+    b = None if bias is None else _vector("bias", bias, N, dtype, device)
+    r, ldr = (None, 0) if residual is None else _operand("residual", residual, (M, N), dtype, device)
+    with _on_device(device, torch):
+        out, y, ldy = _result("out", out, (M, N), dtype, device, torch)
+        z, ldz = None, 0
+        if keep_pre or pre is not None:
+            pre, z, ldz = _result("pre", pre, (M, N), dtype, device, torch)
+        st = _load().sgemm_linear(code, M, N, K, x, ldx, w, ldw, b, r, ldr, act, y, ldy, z, ldz,
+                                  _stream_handle(stream, device, torch))
+    if st != 0:
+        raise SgemmError(st)
+    return (out, pre) if keep_pre else out
+
+
+def linear_backward(dY, X, W, Z=None, *, act: int = ACT_NONE, need_x: bool = True,
+                    need_w: bool = True, need_bias: bool = True, stream=None):
+    """(dX, dW, db): the gradients of ``linear`` for the gradient dY of its
+    result (sgemm_linear_backward); None in the place of one that is not
+    needed.  Z is the activation's input that ``linear(keep_pre=True)`` returned
+    (not needed for ACT_NONE); the gradient of a residual is dY itself.  Types,
+    layout and stream handling as linear()."""
+    import torch
+
+    code = _type_code("dY", dY, torch)
+    if dY.dim() != 2 or X.dim() != 2 or W.dim() != 2:
+        raise ValueError("dY, X and W must be 2-D")
+    dtype, device = dY.dtype, dY.device
+    M, N = dY.shape
+    K = X.shape[1]
+    g, ldg = _operand("dY", dY, (M, N), dtype, device)
+    x, ldx = _operand("X", X, (M, K), dtype, device)
+    w, ldw = _operand("W", W, (N, K), dtype, device)
+    z, ldz = None, max(N, 1)
+    if act != ACT_NONE:
+        if Z is None:
+            raise ValueError("an activation's gradient needs its input Z")
+        z, ldz = _operand("Z", Z, (M, N), dtype, device)
+    dX = dW = db = px = pw = pb = None
+    ldk = max(K, 1)
+    with _on_device(device, torch):
+        if need_x:
+            dX = torch.empty((M, K), dtype=dtype, device=device)
+            px = dX.data_ptr() or None
+        if need_w:
+            dW = torch.empty((N, K), dtype=dtype, device=device)
+            pw = dW.data_ptr() or None
+        if need_bias:
+            db = torch.empty((N,), dtype=dtype, device=device)
+            pb = db.data_ptr() or None
+        st = _load().sgemm_linear_backward(code, M, N, K, g, ldg, z, ldz, act, x, ldx, w, ldw, px,
+                                           ldk, pw, ldk, pb, _stream_handle(stream, device, torch))
+    if st != 0:
+        raise SgemmError(st)
+    return dX, dW, db
+
+
+def _stack(name, t, shape, dtype, device):
+    """(address, leading dimension, matrix stride) of a stack of matrices."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be {dtype} on {device}")
+    step, ld, one = t.stride()
+    if shape[2] > 1 and one != 1:
+        raise ValueError(f"{name}: rows must be contiguous (stride(2) == 1)")
+    return t.data_ptr(), ld if shape[1] > 1 else max(ld, shape[2]), step if shape[0] > 1 else 0
+
+
+def moe(X, router, W1, W2, top_k: int, *, act: int = ACT_SILU, renormalize: bool = True, out=None,
+        return_routing: bool = False, stream=None):
+    """A whole mixture-of-experts layer for at most 64 tokens (sgemm_moe): X is
+    T x D, router E x D, W2 E x D x F, and W1 E x 2F x D (gate rows, then up
+    rows: h = act(gate) * up) or E x F x D (h = act(W1 x)); float32, bfloat16 or
+    float16, one type, rows contiguous.  Each token goes through its top_k
+    experts of largest logit (ties: the lowest index), weighted by the softmax
+    over all experts, divided by the sum of the chosen with renormalize.
+    Returns Y (T x D; ``out`` when given), with return_routing (Y, ids, weights),
+    T x top_k int32 and float32.  Runs asynchronously on ``stream``
+    (default: the current stream of X's device)."""
+    import torch
+
+    code = _type_code("X", X, torch)
+    if X.dim() != 2 or router.dim() != 2 or W1.dim() != 3 or W2.dim() != 3:
+        raise ValueError("X and router must be 2-D, W1 and W2 3-D")
+    dtype, device = X.dtype, X.device
+    T, D = X.shape
+    E, F = W2.shape[0], W2.shape[2]
+    gated = int(W1.shape[1] == 2 * F)
+    x, ldx = _operand("X", X, (T, D), dtype, device)
+    wr, ldr = _operand("router", router, (E, D), dtype, device)
+    w1, ld1, step1 = _stack("W1", W1, (E, 2 * F if gated else F, D), dtype, device)
+    w2, ld2, step2 = _stack("W2", W2, (E, D, F), dtype, device)
+    ids = weights = pi = pw = None
+    with _on_device(device, torch):
+        out, y, ldy = _result("out", out, (T, D), dtype, device, torch)
+        if return_routing:
+            ids = torch.empty((T, top_k), dtype=torch.int32, device=device)
+            weights = torch.empty((T, top_k), dtype=torch.float32, device=device)
+            pi, pw = ids.data_ptr() or None, weights.data_ptr() or None
+        st = _load().sgemm_moe(code, T, D, F, E, top_k, gated, int(bool(renormalize)), act, x, ldx,
+                               wr, ldr, w1, ld1, step1, w2, ld2, step2, y, ldy, pi, pw,
+                               _stream_handle(stream, device, torch))
+    if st != 0:
+        raise SgemmError(st)
+    return (out, ids, weights) if return_routing else out

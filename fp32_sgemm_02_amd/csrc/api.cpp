@@ -863,6 +863,17 @@ const char *sgemm_status_string(int status) {
     case -31: return "the plan's partial sums need more memory than the static scratch holds";
     default: break;
     }
+    if (status <= -101 && status >= -123) {
+        // the feed-forward operators: the argument's number
+        static const char *const text[] = {
+            "invalid argument 1",  "invalid argument 2",  "invalid argument 3",  "invalid argument 4",
+            "invalid argument 5",  "invalid argument 6",  "invalid argument 7",  "invalid argument 8",
+            "invalid argument 9",  "invalid argument 10", "invalid argument 11", "invalid argument 12",
+            "invalid argument 13", "invalid argument 14", "invalid argument 15", "invalid argument 16",
+            "invalid argument 17", "invalid argument 18", "invalid argument 19", "invalid argument 20",
+            "invalid argument 21", "invalid argument 22", "invalid argument 23"};
+        return text[-101 - status];
+    }
     if (status > 0) return hipGetErrorString(static_cast<hipError_t>(status));
     return "unknown status";
 }

@@ -112,7 +112,10 @@ struct Workspace {
     void *base = nullptr;           // the allocation (graph capture)
     bool owned = false;             // allocated for this call (graph capture)
 };
-hipError_t workspace_acquire(size_t bytes, hipStream_t stream, const Problem &p, Workspace &w);
+// kind: buffers of different kinds are cached apart (0: the products' partial
+// sums; 1: the feed-forward operators, several launches of which share one).
+hipError_t workspace_acquire(size_t bytes, hipStream_t stream, const Problem &p, Workspace &w,
+                             int kind = 0);
 hipError_t workspace_release(const Workspace &w, hipStream_t stream);
 hipError_t workspace_release_all();   // the current device's cached buffers
 // The static scratch array of the current device (workspace.cpp): its device

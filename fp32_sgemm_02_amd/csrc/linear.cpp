@@ -1,0 +1,286 @@
+// linear.cpp -- the C ABI of the feed-forward operators: linear layers with
+// their whole epilogue, their backward pass, and the mixture-of-experts layer.
+// Argument checks, empty cases, the choice of kernels, and their launches.
+//
+// A call makes up to three launches that hand data to each other through the
+// workspace of its stream, and calls of several host threads may meet on one
+// stream: the launches of a call are made under a lock, so that they stay
+// together in the stream's order.
+#include <cstdint>
+#include <mutex>
+
+#include "linear_internal.hpp"
+
+namespace sg {
+namespace {
+
+constexpr int bad(int argument) { return -100 - argument; }
+
+int to_status(hipError_t e) { return (int)e; }
+
+int elem_of(int dtype) { return dtype == SGEMM_DTYPE_F32 ? 4 : 2; }
+bool known(int dtype) {
+    return dtype == SGEMM_DTYPE_F32 || dtype == SGEMM_DTYPE_BF16 || dtype == SGEMM_DTYPE_F16;
+}
+bool aligned(const void *q, int to) { return reinterpret_cast<uintptr_t>(q) % to == 0; }
+bool usable(const void *q, int elem) { return q && aligned(q, elem); }
+size_t round_up(size_t v, size_t to) { return (v + to - 1) / to * to; }
+
+std::mutex &launch_mutex() {
+    static std::mutex m;
+    return m;
+}
+
+// The feed-forward workspace of a call: acquired (where bytes are needed),
+// used by the launches of f, and released.
+template <class F>
+int with_workspace(size_t bytes, bool counters, hipStream_t stream, F &&f) {
+    std::lock_guard<std::mutex> lock(launch_mutex());
+    Workspace ws;
+    if (bytes || counters) {
+        const hipError_t e = workspace_acquire(bytes, stream, Problem{}, ws, 1);
+        if (e != hipSuccess) return to_status(e);
+    }
+    int st = f(ws);
+    const hipError_t e = workspace_release(ws, stream);
+    return st != 0 ? st : to_status(e);
+}
+
+// Part of a workspace: the same counters, the sums from `offset` bytes on.
+Workspace part_of(const Workspace &ws, size_t offset) {
+    Workspace w = ws;
+    w.ptr = static_cast<unsigned char *>(ws.ptr) + offset;
+    return w;
+}
+
+size_t product_workspace(int dtype, const Prod &p, bool rows) {
+    return rows ? rows_workspace(dtype, p) : prod16_workspace(dtype, p);
+}
+hipError_t launch_product(int dtype, const Prod &p, bool rows, const Workspace &ws,
+                          hipStream_t stream) {
+    return rows ? launch_rows(dtype, p, ws, stream) : launch_prod16(dtype, p, ws, stream);
+}
+
+int run_linear(int dtype, const Prod &p, hipStream_t stream) {
+    const bool rows = p.M <= kFewRows;
+    if (dtype != SGEMM_DTYPE_F32 || rows) {
+        const size_t bytes = product_workspace(dtype, p, rows);
+        return with_workspace(bytes, false, stream, [&](const Workspace &ws) {
+            return to_status(launch_product(dtype, p, rows, ws, stream));
+        });
+    }
+    // fp32: the library's product with the bias in its epilogue, then one
+    // elementwise pass for what comes after the sum
+    const float *A = static_cast<const float *>(p.A), *B = static_cast<const float *>(p.B);
+    const float *bias = static_cast<const float *>(p.bias), *R = static_cast<const float *>(p.R);
+    float *Y = static_cast<float *>(p.C), *Z = static_cast<float *>(p.Z);
+    auto product = [&](float *C, int ldc, int act) {
+        return sgemm_epilogue(0, 1, p.M, p.N, p.K, 1.f, A, (int)p.lda, B, (int)p.ldb, 0.f, C, ldc,
+                              bias, act, stream);
+    };
+    if (!R && !Z) return product(Y, (int)p.ldc, p.act);
+    if (Z) {
+        const int st = product(Z, (int)p.ldz, SGEMM_ACT_NONE);
+        return st != 0 ? st
+                       : to_status(launch_finish32(p.M, p.N, Z, p.ldz, p.act, R, p.ldr, Y, p.ldc,
+                                                   stream));
+    }
+    const size_t ld = round_up(p.N, 4);
+    return with_workspace(ld * p.M * 4, false, stream, [&](const Workspace &ws) {
+        float *t = static_cast<float *>(ws.ptr);
+        const int st = product(t, (int)ld, p.act);
+        return st != 0 ? st
+                       : to_status(launch_finish32(p.M, p.N, t, ld, SGEMM_ACT_NONE, R, p.ldr, Y,
+                                                   p.ldc, stream));
+    });
+}
+
+struct Backward {
+    int M, N, K;
+    const void *dY;
+    int lddy;
+    const void *Z;
+    int ldz, act;
+    const void *X;
+    int ldx;
+    const void *W;
+    int ldw;
+    void *dX;
+    int lddx;
+    void *dW;
+    int lddw;
+    void *db;
+};
+
+int run_backward(int dtype, const Backward &b, hipStream_t stream) {
+    const int elem = elem_of(dtype), v = 16 / elem;
+    const bool f32 = dtype == SGEMM_DTYPE_F32;
+    const bool want_dx = b.dX && b.M > 0 && b.K > 0, want_dw = b.dW && b.N > 0 && b.K > 0;
+    const bool want_db = b.db && b.N > 0;
+    const bool few = b.M <= kFewRows;
+    // G is dY itself without an activation, as long as the 16-bit tiles can
+    // load its rows directly
+    const bool g_is_dy = b.act == SGEMM_ACT_NONE &&
+                         (f32 || (rows16(b.dY, b.lddy, elem) && b.N % v == 0));
+    const bool make_g = !g_is_dy && (want_dx || want_dw) && b.M > 0 && b.N > 0;
+    // few rows: both products are bound by W and dW, so G is kept in two parts
+    // (as exact as fp32) at no cost; otherwise its rounding adds an error of
+    // the size of the results' own rounding
+    const bool two = make_g && few && !f32 && b.act != SGEMM_ACT_NONE;
+    const long long ldg = make_g ? (long long)round_up(b.N, v) : b.lddy;
+    const size_t g_bytes =
+        make_g ? round_up((size_t)(two ? 2 * kFewRows : b.M) * ldg * elem, 256) : 0;
+
+    Prod dx{b.M, b.K, b.N, b.dY, ldg, b.W, b.ldw, b.dX, b.lddx};
+    dx.b_mc = 1;
+    Prod dw{b.N, b.K, b.M, b.dY, ldg, b.X, b.ldx, b.dW, b.lddw};
+    dw.a_mc = dw.b_mc = 1;
+    dx.a_pad = dw.a_pad = make_g;
+    dw.fold = two;
+    const bool dx_ours = want_dx && (!f32 || few), dw_ours = want_dw && !f32;
+    size_t scratch = want_db ? grad_workspace(dtype, b.M, b.N) : 0;
+    if (dx_ours) {
+        const size_t s = product_workspace(dtype, dx, few);
+        if (s > scratch) scratch = s;
+    }
+    if (dw_ours) {
+        const size_t s = product_workspace(dtype, dw, false);
+        if (s > scratch) scratch = s;
+    }
+    return with_workspace(g_bytes + scratch, false, stream, [&](const Workspace &ws) -> int {
+        const Workspace rest = ws.ptr ? part_of(ws, g_bytes) : ws;
+        if (make_g || want_db) {
+            unsigned char *G = make_g ? static_cast<unsigned char *>(ws.ptr) : nullptr;
+            void *lo = two ? G + (size_t)kFewRows * ldg * elem : nullptr;
+            const hipError_t e =
+                launch_grad(dtype, b.M, b.N, b.dY, b.lddy, b.Z, b.ldz, b.act, G, lo, ldg,
+                            want_db ? b.db : nullptr, static_cast<float *>(rest.ptr),
+                            rest.counters, stream);
+            if (e != hipSuccess) return to_status(e);
+            if (make_g) dx.A = dw.A = G;
+            dx.lo = lo;
+        }
+        if (want_dx) {
+            int st;
+            if (dx_ours)
+                st = to_status(launch_product(dtype, dx, few, rest, stream));
+            else
+                st = sgemm_op(0, 0, b.M, b.K, b.N, 1.f, static_cast<const float *>(dx.A), (int)ldg,
+                              static_cast<const float *>(b.W), b.ldw, 0.f,
+                              static_cast<float *>(b.dX), b.lddx, stream);
+            if (st != 0) return st;
+        }
+        if (want_dw) {
+            if (dw_ours) return to_status(launch_product(dtype, dw, false, rest, stream));
+            return sgemm_op(1, 0, b.N, b.K, b.M, 1.f, static_cast<const float *>(dw.A), (int)ldg,
+                            static_cast<const float *>(b.X), b.ldx, 0.f,
+                            static_cast<float *>(b.dW), b.lddw, stream);
+        }
+        return 0;
+    });
+}
+
+}  // namespace
+}  // namespace sg
+
+extern "C" {
+
+int sgemm_linear(int dtype, int M, int N, int K, const void *X, int ldx, const void *W, int ldw,
+                 const void *bias, const void *R, int ldr, int act, void *Y, int ldy, void *Z,
+                 int ldz, hipStream_t stream) {
+    using namespace sg;
+    if (!known(dtype)) return bad(1);
+    const int elem = elem_of(dtype);
+    if (M < 0) return bad(2);
+    if (N < 0) return bad(3);
+    if (K < 0) return bad(4);
+    if (ldx < (K > 1 ? K : 1)) return bad(6);
+    if (ldw < (K > 1 ? K : 1)) return bad(8);
+    if (bias && !aligned(bias, elem)) return bad(9);
+    if (R && !aligned(R, elem)) return bad(10);
+    if (R && ldr < (N > 1 ? N : 1)) return bad(11);
+    if (act < SGEMM_ACT_NONE || act > SGEMM_ACT_GELU_TANH) return bad(12);
+    if (ldy < (N > 1 ? N : 1)) return bad(14);
+    if (Z && !aligned(Z, elem)) return bad(15);
+    if (Z && ldz < (N > 1 ? N : 1)) return bad(16);
+    if (M == 0 || N == 0) return 0;
+    if (K > 0 && !usable(X, elem)) return bad(5);
+    if (K > 0 && !usable(W, elem)) return bad(7);
+    if (!usable(Y, elem)) return bad(13);
+    Prod p{M, N, K, X, ldx, W, ldw, Y, ldy};
+    p.bias = bias;
+    p.R = R;
+    p.ldr = ldr;
+    p.Z = Z;
+    p.ldz = ldz;
+    p.act = act;
+    return run_linear(dtype, p, stream);
+}
+
+int sgemm_linear_backward(int dtype, int M, int N, int K, const void *dY, int lddy, const void *Z,
+                          int ldz, int act, const void *X, int ldx, const void *W, int ldw,
+                          void *dX, int lddx, void *dW, int lddw, void *db, hipStream_t stream) {
+    using namespace sg;
+    if (!known(dtype)) return bad(1);
+    const int elem = elem_of(dtype);
+    if (M < 0) return bad(2);
+    if (N < 0) return bad(3);
+    if (K < 0) return bad(4);
+    const int n1 = N > 1 ? N : 1, k1 = K > 1 ? K : 1;
+    if (lddy < n1) return bad(6);
+    if (act < SGEMM_ACT_NONE || act > SGEMM_ACT_GELU_TANH) return bad(9);
+    const bool cells = M > 0 && N > 0;
+    if (cells && !usable(dY, elem)) return bad(5);
+    if (cells && act != SGEMM_ACT_NONE && !usable(Z, elem)) return bad(7);
+    if (act != SGEMM_ACT_NONE && ldz < n1) return bad(8);
+    if (dW && ldx < k1) return bad(11);
+    if (dW && cells && K > 0 && !usable(X, elem)) return bad(10);
+    if (dX && ldw < k1) return bad(13);
+    if (dX && cells && K > 0 && !usable(W, elem)) return bad(12);
+    if (dX && !aligned(dX, elem)) return bad(14);
+    if (dX && lddx < k1) return bad(15);
+    if (dW && !aligned(dW, elem)) return bad(16);
+    if (dW && lddw < k1) return bad(17);
+    if (db && !aligned(db, elem)) return bad(18);
+    const Backward b{M, N, K, dY, lddy, Z, ldz, act, X, ldx, W, ldw, dX, lddx, dW, lddw, db};
+    return run_backward(dtype, b, stream);
+}
+
+int sgemm_moe(int dtype, int T, int D, int F, int E, int top_k, int gated, int renormalize, int act,
+              const void *X, int ldx, const void *Wr, int ldr, const void *W1, int ld1,
+              long long stride1, const void *W2, int ld2, long long stride2, void *Y, int ldy,
+              int *ids, float *weights, hipStream_t stream) {
+    using namespace sg;
+    if (!known(dtype)) return bad(1);
+    const int elem = elem_of(dtype);
+    if (T < 0 || T > kMoeTokens) return bad(2);
+    if (D < 1 || D > 16 * (kWorkspaceCounters - kMoeTokens)) return bad(3);
+    if (F < 1 || F > (1 << 20)) return bad(4);
+    if (E < 1 || E > kMoeExperts) return bad(5);
+    if (top_k < 1 || top_k > kMoeChoices || top_k > E) return bad(6);
+    if (gated != 0 && gated != 1) return bad(7);
+    if (renormalize != 0 && renormalize != 1) return bad(8);
+    if (act < SGEMM_ACT_NONE || act > SGEMM_ACT_GELU_TANH) return bad(9);
+    if (ldx < D) return bad(11);
+    if (ldr < D) return bad(13);
+    if (ld1 < D) return bad(15);
+    if (stride1 < 0) return bad(16);
+    if (ld2 < F) return bad(18);
+    if (stride2 < 0) return bad(19);
+    if (ldy < D) return bad(21);
+    if (ids && !aligned(ids, 4)) return bad(22);
+    if (weights && !aligned(weights, 4)) return bad(23);
+    if (T == 0) return 0;
+    if (!usable(X, elem)) return bad(10);
+    if (!usable(Wr, elem)) return bad(12);
+    if (!usable(W1, elem)) return bad(14);
+    if (!usable(W2, elem)) return bad(17);
+    if (!usable(Y, elem)) return bad(20);
+    const Moe m{T,  D,   F,   E,       top_k, gated, renormalize, act,     X, ldx, Wr, ldr,
+                W1, ld1, stride1, W2,  ld2,   stride2, Y,         ldy, ids, weights};
+    return with_workspace(moe_workspace(dtype, m), true, stream, [&](const Workspace &ws) {
+        return to_status(launch_moe(dtype, m, ws, stream));
+    });
+}
+
+}  // extern "C"

@@ -1,0 +1,374 @@
+// linear16.hip -- products of 16-bit operands with a 16-bit result and the
+// whole epilogue of a linear layer in the kernel.
+//
+//     C(m, n) = act(sum_k A(m, k) B(n, k) + bias(n)) + R(m, n)
+//
+// The three products of a linear layer are this one with different storage:
+//     Y  = X W^T    A = X (k contiguous),  B = W (k contiguous)
+//     dX = G W      A = G (k contiguous),  B = W read with its own index
+//                   contiguous (k walks the rows of W)
+//     dW = G^T X    A = G and B = X, both with their own index contiguous
+//
+// Operand images in LDS.  A stage is 64 values of k.  A k-contiguous operand
+// is held as rows of 128 bytes, the eight 16-byte chunks of a row swizzled
+// (chunk c of row r in slot c ^ (r >> 1 & 7)), and a lane's MFMA fragment is
+// one 16-byte read.  The other kind is held as 64 rows (one per k) of the
+// tile's width and read with the transposing LDS read: in a group of 16 lanes,
+// lane j fetches four values of row j / 4 and receives, as its four results,
+// value i = j of those four rows, so two reads give the 8 k values of a
+// fragment.  The chunks of those rows are swizzled by k (mc_swz) so that the
+// 16 lanes of a group touch 16 different bank pairs.
+//
+// Row order.  MFMA row and column indices are free labels, so index i of block
+// b within a group of G blocks stands for row 4G (i / 4) + 4b + i % 4 of the
+// group: a lane then holds 4G adjacent columns of one row of C over the G
+// blocks, and stores them 16 bytes at a time.
+#include "linear_internal.hpp"
+
+namespace sg {
+namespace {
+
+typedef __attribute__((address_space(3))) void lds_void;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef s16x4 __attribute__((address_space(3))) lds_s16x4;
+
+constexpr int kBK = 64;                            // k per stage
+constexpr int kOutOfRange = (int)0x80000000u;      // a buffer offset that reads zero
+
+template <int N>
+__device__ __forceinline__ void wait_vmcnt() {
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+
+// Tile row held in image row r, groups of G 16-row blocks.
+template <int G>
+__device__ __forceinline__ int image_row(int r) {
+    return (r & ~(16 * G - 1)) | (4 * G * ((r & 15) >> 2) + 4 * ((r >> 4) & (G - 1)) + (r & 3));
+}
+
+// Swizzle of the 16-byte chunks of row k of an own-index-contiguous image of
+// BT columns read in groups of G blocks: the four rows of one transposing read
+// (k mod 4) are moved to chunks that the others' reads do not touch.
+template <int BT, int G>
+__device__ __forceinline__ int mc_swz(int k) {
+    constexpr int C = BT / 8;   // chunks per row
+    if constexpr (C >= 16)
+        return G == 4 ? ((k & 1) | ((k & 2) << 2)) : G == 2 ? ((k & 3) << 2) : ((k & 3) << 1);
+    else if constexpr (C == 8)   // rows of 128 bytes: neighbours are 128 bytes apart already
+        return G == 4 ? ((k >> 1) & 1) : G == 2 ? (((k >> 1) & 1) << 2) : (((k >> 1) & 1) << 1);
+    else
+        return 0;
+}
+
+// One operand's tile: BT rows, stored k-contiguous (MC = 0) or with its own
+// index contiguous (MC = 1), read in groups of G blocks by NW waves' loads.
+// DIRECT: 16-byte rows throughout, copied to LDS by direct loads (a chunk
+// outside the matrix reads as zero: its buffer offset is out of range).
+// Otherwise the chunks pass through registers, from any 2-byte alignment
+// (the target loads 16 bytes from any address), those that straddle an edge
+// value by value.
+template <int BT, int MC, bool DIRECT, int G, int NW>
+struct Operand {
+    static constexpr int BYTES = BT * kBK * 2;
+    static constexpr int L = BT * 8 / (64 * NW);   // 16-byte chunks per lane and stage
+    static_assert(L * 64 * NW == BT * 8, "chunks divide evenly");
+
+    int off[L];   // DIRECT: byte offset from the stage's origin; else row of the chunk
+    int kk[L];    // k of the chunk within the stage
+    int cc[L];    // !DIRECT, MC: first tile column of the chunk
+    const u16 *base;
+    long long ld;
+    int lim;   // rows of the tile inside the matrix
+    uintx4 reg[DIRECT ? 1 : L];
+
+    __device__ __forceinline__ void init(const u16 *P, long long ld_, int row0, int rows, int wave,
+                                         int lane) {
+        ld = ld_;
+        lim = rows - row0;
+        base = MC ? P + row0 : P + (long long)row0 * ld;
+#pragma unroll
+        for (int j = 0; j < L; ++j) {
+            const int q = (j * NW + wave) * 64 + lane;   // chunk of the image
+            if constexpr (MC) {
+                const int k = q / (BT / 8), c = (q % (BT / 8)) ^ mc_swz<BT, G>(k);
+                kk[j] = k;
+                cc[j] = 8 * c;
+                off[j] = 8 * c >= lim ? kOutOfRange : (k * (int)ld + 8 * c) * 2;
+            } else {
+                const int r = q / 8, c = (q % 8) ^ ((r >> 1) & 7), row = image_row<G>(r);
+                kk[j] = 8 * c;
+                cc[j] = row;
+                off[j] = row >= lim ? kOutOfRange : (row * (int)ld + 8 * c) * 2;
+            }
+        }
+    }
+
+    // Copy of stage t into the image (DIRECT) or into registers; krem: k values
+    // of the stage inside the matrix.
+    __device__ __forceinline__ void issue(int t, int krem, unsigned char *img, int wave) {
+        const u16 *src = MC ? base + (long long)t * kBK * ld : base + (long long)t * kBK;
+        if constexpr (DIRECT) {
+            const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+                (void *)src, (short)0, 0x7fffffff, 0x00020000);
+#pragma unroll
+            for (int j = 0; j < L; ++j)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    r, (lds_void *)(img + (j * NW + wave) * 1024), 16,
+                    kk[j] >= krem ? kOutOfRange : off[j], 0, 0, 0);
+        } else {
+#pragma unroll
+            for (int j = 0; j < L; ++j) {
+                const int n = MC ? (kk[j] < krem ? lim - cc[j] : 0)
+                                 : (cc[j] < lim ? krem - kk[j] : 0);   // values inside
+                const u16 *s = MC ? src + (long long)kk[j] * ld + cc[j]
+                                  : src + (long long)cc[j] * ld + kk[j];
+                uintx4 v = {0, 0, 0, 0};
+                if (n >= 8) {
+                    __builtin_memcpy(&v, s, 16);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (e < n) v[e / 2] |= (unsigned)s[e] << (16 * (e & 1));
+                }
+                reg[j] = v;
+            }
+        }
+    }
+    __device__ __forceinline__ void commit(unsigned char *img, int wave, int lane) {
+        if constexpr (!DIRECT) {
+#pragma unroll
+            for (int j = 0; j < L; ++j)
+                *reinterpret_cast<uintx4 *>(img + ((j * NW + wave) * 64 + lane) * 16) = reg[j];
+        }
+    }
+
+    // Fragment of 16-row block `blk` (counted from the tile's first row) and
+    // 32-k step s.
+    static __device__ __forceinline__ uintx4 frag(const unsigned char *img, int blk, int s,
+                                                  int lane) {
+        const int i = lane & 15, g = lane >> 4;
+        if constexpr (MC) {
+            const int col = 16 * G * (blk / G) + 4 * G * (i & 3) + 4 * (blk % G);
+            const int k = 32 * s + 8 * g + (i >> 2);   // and k + 4: the same swizzle
+            const int at = k * (BT * 2) + (((col >> 3) ^ mc_swz<BT, G>(k)) << 4) + ((col & 4) << 1);
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(img + at));
+            const s16x4 hi =
+                __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(img + at + 4 * BT * 2));
+            const uintx2 l = __builtin_bit_cast(uintx2, lo), h = __builtin_bit_cast(uintx2, hi);
+            return uintx4{l[0], l[1], h[0], h[1]};
+        } else {
+            const int r = 16 * blk + i;
+            return *reinterpret_cast<const uintx4 *>(img + r * 128 +
+                                                     (((4 * s + g) ^ ((r >> 1) & 7)) << 4));
+        }
+    }
+};
+
+struct Grid16 {
+    int tiles_m, tiles_n, group_m;
+    int slices, per;     // k slices, stages per slice
+    float *part;         // slices x tiles x the tile's accumulators
+    unsigned *count;     // one arrival counter per tile, zero between launches
+};
+
+// Split over k: the workgroup leaves its accumulators in memory and the one
+// that counts last adds the slices in order.  Returns whether this workgroup
+// finishes the tile (its acc then holds the whole sum).
+template <int NB, int MB, int NT>
+__device__ __forceinline__ bool join_slices(const Grid16 &gr, int tile, int tiles, int slice,
+                                            int tid, floatx4 (&acc)[NB][MB]) {
+    __shared__ int last;
+    auto at = [&](int s, int j) {
+        return gr.part + ((((long long)s * tiles + tile) * (NB * MB) + j) * NT + tid) * 4;
+    };
+#pragma unroll
+    for (int j = 0; j < NB * MB; ++j) store_partial(at(slice, j), acc[j / MB][j % MB]);
+    if (!arrive_last(gr.count + tile, gr.slices, &last)) return false;
+#pragma unroll
+    for (int j = 0; j < NB * MB; ++j) acc[j / MB][j % MB] = load_partial(at(0, j));
+    for (int s = 1; s < gr.slices; ++s)
+#pragma unroll
+        for (int j = 0; j < NB * MB; ++j) {
+            const floatx4 v = load_partial(at(s, j));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[j / MB][j % MB][e] += v[e];
+        }
+    if (tid == 0) __hip_atomic_store(gr.count + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return true;
+}
+
+// The tile kernel: BM x BN of C per workgroup, WM x WN per wave, two stages in
+// LDS, one barrier per stage.
+template <int DT, int BM, int BN, int WM, int WN, int AMC, int BMC, bool ADIR, bool BDIR>
+__global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN))
+prod16_kernel(Prod p, Grid16 gr) {
+#ifdef __HIP_DEVICE_COMPILE__   // the host pass needs the launch stub only
+    constexpr int WAVES_N = BN / WN, NW = (BM / WM) * WAVES_N, NT = 64 * NW;
+    constexpr int MB = WM / 16, NB = WN / 16;
+    constexpr int GM = MB < 4 ? MB : 4, GN = NB < 4 ? NB : 4;
+    using OpA = Operand<BM, AMC, ADIR, GM, NW>;
+    using OpB = Operand<BN, BMC, BDIR, GN, NW>;
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[2][OpA::BYTES + OpB::BYTES];
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / WAVES_N, wn = wave % WAVES_N;
+    const int tiles = gr.tiles_m * gr.tiles_n;
+    const int slice = blockIdx.y;
+    int tm, tn;
+    const int tile = xcd_remap(blockIdx.x, tiles);
+    tile_coords(tile, gr.tiles_m, gr.tiles_n, gr.group_m, tm, tn);
+    const int m0 = tm * BM, n0 = tn * BN;
+    const int stages = p.fold ? 2 : (p.K + kBK - 1) / kBK;
+    const int t0 = slice * gr.per, t1 = min(t0 + gr.per, stages);
+
+    OpA a;
+    OpB b;
+    a.init(static_cast<const u16 *>(p.A), p.lda, m0, p.M, wave, lane);
+    b.init(static_cast<const u16 *>(p.B), p.ldb, n0, p.N, wave, lane);
+
+    floatx4 acc[NB][MB];
+#pragma unroll
+    for (int y = 0; y < NB; ++y)
+#pragma unroll
+        for (int x = 0; x < MB; ++x) acc[y][x] = floatx4{0.f, 0.f, 0.f, 0.f};
+
+    auto issue = [&](int t, unsigned char *img) {
+        const int krem = p.fold ? p.K : p.K - t * kBK;
+        a.issue(t, krem, img, wave);
+        b.issue(p.fold ? 0 : t, krem, img + OpA::BYTES, wave);
+    };
+    if (t0 < t1) issue(t0, smem[0]);
+    for (int t = t0; t < t1; ++t) {
+        unsigned char *cur = smem[(t - t0) & 1], *nxt = smem[(t - t0 + 1) & 1];
+        a.commit(cur, wave, lane);
+        b.commit(cur + OpA::BYTES, wave, lane);
+        wait_vmcnt<0>();
+        __syncthreads();   // stage t is in LDS, and no wave reads the other buffer
+        if (t + 1 < t1) issue(t + 1, nxt);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            uintx4 fa[MB], fb[NB];
+#pragma unroll
+            for (int x = 0; x < MB; ++x) fa[x] = OpA::frag(cur, wm * MB + x, s, lane);
+#pragma unroll
+            for (int y = 0; y < NB; ++y) fb[y] = OpB::frag(cur + OpA::BYTES, wn * NB + y, s, lane);
+#pragma unroll
+            for (int y = 0; y < NB; ++y)
+#pragma unroll
+                for (int x = 0; x < MB; ++x) acc[y][x] = mfma16<DT>(fb[y], fa[x], acc[y][x]);
+        }
+    }
+    if (gr.slices > 1 && !join_slices<NB, MB, NT>(gr, tile, tiles, slice, tid, acc)) return;
+
+    const int i = lane & 15, g = lane >> 4;
+    with_act(p.act, [&](auto tag) {
+        constexpr int ACT = decltype(tag)::value;
+#pragma unroll
+        for (int x = 0; x < MB; ++x) {
+            const int m = m0 + wm * WM + 16 * GM * (x / GM) + 4 * GM * (i >> 2) + 4 * (x % GM) + (i & 3);
+            if (m >= p.M) continue;
+#pragma unroll
+            for (int q = 0; q < NB / GN; ++q) {
+                float v[4 * GN];
+#pragma unroll
+                for (int y = 0; y < GN; ++y)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) v[4 * y + r] = acc[q * GN + y][x][r];
+                finish_run<DT, ACT>(p, m, n0 + wn * WN + 16 * GN * q + 4 * GN * g, v);
+            }
+        }
+    });
+#endif
+}
+
+// ---- host: tile and split --------------------------------------------------
+
+// Whether an operand's rows take direct 16-byte loads: 16-byte rows whose
+// stored length is whole chunks, and a tile whose byte offsets fit 31 bits.
+bool direct_ok(const void *q, long long ld, int row_len, int bt, int mc) {
+    return rows16(q, ld, 2) && row_len % 8 == 0 && (mc ? kBK : bt) * ld * 2 < 0x7fff0000LL;
+}
+
+struct Plan16 {
+    int bm, bn, slices, per;
+};
+
+constexpr int kCUs = 256;
+
+Plan16 plan16(const Prod &p) {
+    auto tiles = [&](int b) { return (long long)((p.M + b - 1) / b) * ((p.N + b - 1) / b); };
+    Plan16 q;
+    q.bm = q.bn = tiles(128) >= kCUs ? 128 : 64;
+    const long long t = tiles(q.bm);
+    const int stages = p.fold ? 2 : (p.K + kBK - 1) / kBK;
+    int s = 1;
+    if (!p.fold && t < 2 * kCUs && t <= kWorkspaceCounters) {
+        s = (int)((2 * kCUs + t - 1) / t);
+        const int most = stages / 4;
+        if (s > most) s = most;
+        if (s > 32) s = 32;
+        if (s < 1) s = 1;
+    }
+    q.per = (stages + s - 1) / s;
+    if (q.per < 1) q.per = 1;
+    q.slices = stages ? (stages + q.per - 1) / q.per : 1;
+    return q;
+}
+
+template <int DT, int BM, int BN, int WM, int WN, int AMC, int BMC>
+hipError_t launch_tile(const Prod &p, const Grid16 &gr, bool ad, bool bd, hipStream_t stream) {
+    constexpr int NT = 64 * (BM / WM) * (BN / WN);
+    const dim3 grid(gr.tiles_m * gr.tiles_n, gr.slices);
+    if (ad && bd)
+        hipLaunchKernelGGL((prod16_kernel<DT, BM, BN, WM, WN, AMC, BMC, true, true>), grid,
+                           dim3(NT), 0, stream, p, gr);
+    else if (ad && BMC)   // the backward products: G is laid out for direct loads, B may not be
+        hipLaunchKernelGGL((prod16_kernel<DT, BM, BN, WM, WN, AMC, BMC, BMC != 0, false>), grid,
+                           dim3(NT), 0, stream, p, gr);
+    else
+        hipLaunchKernelGGL((prod16_kernel<DT, BM, BN, WM, WN, AMC, BMC, false, false>), grid,
+                           dim3(NT), 0, stream, p, gr);
+    return hipGetLastError();
+}
+
+template <int DT, int BM, int BN, int WM, int WN>
+hipError_t launch_layout(const Prod &p, const Grid16 &gr, bool ad, bool bd, hipStream_t stream) {
+    if (!p.b_mc) return launch_tile<DT, BM, BN, WM, WN, 0, 0>(p, gr, ad, bd, stream);
+    if (!p.a_mc) return launch_tile<DT, BM, BN, WM, WN, 0, 1>(p, gr, ad, bd, stream);
+    return launch_tile<DT, BM, BN, WM, WN, 1, 1>(p, gr, ad, bd, stream);
+}
+
+template <int DT>
+hipError_t launch_dt(Prod p, const Workspace &ws, hipStream_t stream) {
+    const Plan16 q = plan16(p);
+    p.cvec = epilogue_vec(p, 2);
+    Grid16 gr{};
+    gr.tiles_m = (p.M + q.bm - 1) / q.bm;
+    gr.tiles_n = (p.N + q.bn - 1) / q.bn;
+    gr.group_m = 8;
+    gr.slices = q.slices;
+    gr.per = q.per;
+    gr.part = static_cast<float *>(ws.ptr);
+    gr.count = ws.counters;
+    const bool ad = direct_ok(p.A, p.lda, p.a_pad ? 0 : p.a_mc ? p.M : p.K, q.bm, p.a_mc);
+    const bool bd = direct_ok(p.B, p.ldb, p.b_mc ? p.N : p.K, q.bn, p.b_mc);
+    if (q.bm == 128) return launch_layout<DT, 128, 128, 64, 64>(p, gr, ad, bd, stream);
+    return launch_layout<DT, 64, 64, 32, 32>(p, gr, ad, bd, stream);
+}
+
+}  // namespace
+
+size_t prod16_workspace(int, const Prod &p) {
+    const Plan16 q = plan16(p);
+    if (q.slices == 1) return 0;
+    const size_t tiles = (size_t)((p.M + q.bm - 1) / q.bm) * ((p.N + q.bn - 1) / q.bn);
+    return tiles * q.slices * q.bm * q.bn * sizeof(float);
+}
+
+hipError_t launch_prod16(int dtype, const Prod &p, const Workspace &ws, hipStream_t stream) {
+    return dtype == SGEMM_DTYPE_BF16 ? launch_dt<SGEMM_DTYPE_BF16>(p, ws, stream)
+                                     : launch_dt<SGEMM_DTYPE_F16>(p, ws, stream);
+}
+
+}  // namespace sg

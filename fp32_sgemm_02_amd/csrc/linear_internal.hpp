@@ -1,0 +1,292 @@
+// linear_internal.hpp -- types shared by the feed-forward operators (linear
+// layers, their backward pass, the mixture-of-experts layer) and the C-ABI
+// entry points of linear.cpp.  Internal to the library.
+#pragma once
+
+#include <type_traits>
+
+#include "gemm_internal.hpp"
+
+namespace sg {
+
+typedef unsigned short u16;
+
+// One product of a linear layer,
+//     C(m, n) = act(sum_k A(m, k) B(n, k) + bias(n)) + R(m, n),
+// all of one type (SGEMM_DTYPE_*), summed and finished in fp32 and rounded
+// once.  Each operand is stored with k contiguous (A(m, k) = A[m * lda + k])
+// or, with a_mc / b_mc, with its own index contiguous (A(m, k) =
+// A[k * lda + m]).  Z, when given, receives the sum plus bias before the
+// activation.  Sizes and leading dimensions in elements.
+struct Prod {
+    int M, N, K;
+    const void *A;
+    long long lda;
+    const void *B;
+    long long ldb;
+    void *C;
+    long long ldc;
+    int a_mc = 0, b_mc = 0;
+    const void *bias = nullptr;
+    const void *R = nullptr;
+    long long ldr = 0;
+    void *Z = nullptr;
+    long long ldz = 0;
+    int act = SGEMM_ACT_NONE;
+    int cvec = 0;   // 16-byte I/O of C, R, Z and bias (set by the launchers)
+    int a_pad = 0;  // the rows of A are filled up with zeros to 16 bytes
+    // What the rounding of A left over, laid out as A (few-rows products only).
+    const void *lo = nullptr;
+    // K <= 64 and A (a_mc) given in two parts whose sum is meant: rows
+    // 0 .. K-1, and rows 64 .. 64+K-1, each summed against the same B.
+    int fold = 0;
+};
+
+// Tile kernels of 16-bit products (linear16.hip): bytes of partial sums (after
+// the workspace's counters) that a launch takes, and the launch.  `ws` may be
+// empty when no bytes are needed.
+size_t prod16_workspace(int dtype, const Prod &p);
+hipError_t launch_prod16(int dtype, const Prod &p, const Workspace &ws, hipStream_t stream);
+
+// Few-rows kernels (linear_rows.hip), M <= kFewRows, every type, A with k
+// contiguous and either B: B is streamed once, from memory into registers.
+constexpr int kFewRows = 64;
+size_t rows_workspace(int dtype, const Prod &p);
+hipError_t launch_rows(int dtype, const Prod &p, const Workspace &ws, hipStream_t stream);
+
+// G = dY * act'(Z) over M x N and its column sums (dtype SGEMM_DTYPE_*): G is
+// written where it is not null (rows of ldg values, 16-byte aligned, zeros from N
+// to the end of its last 16 bytes), rounded to dtype, with what the rounding left
+// over in lo where that is not null; db, where it is not null, receives the
+// sums, rounded to dtype.  They are added in fp32 from the unrounded values in
+// an order that is fixed for a shape.  part: grad_workspace bytes; count:
+// arrival counters, zero between launches.
+size_t grad_workspace(int dtype, int M, int N);
+hipError_t launch_grad(int dtype, int M, int N, const void *dY, long long lddy, const void *Z,
+                       long long ldz, int act, void *G, void *lo, long long ldg, void *db,
+                       float *part, unsigned *count, hipStream_t stream);
+
+// A mixture-of-experts layer for few tokens (moe.hip); see sgemm_moe.
+constexpr int kMoeTokens = 64, kMoeExperts = 512, kMoeChoices = 16;
+struct Moe {
+    int T, D, F, E, k;
+    int gated, renorm, act;
+    const void *X;
+    long long ldx;
+    const void *Wr;
+    long long ldwr;
+    const void *W1;
+    long long ld1, stride1;
+    const void *W2;
+    long long ld2, stride2;
+    void *Y;
+    long long ldy;
+    int *ids;         // T x k, or null
+    float *weights;   // T x k, or null
+};
+size_t moe_workspace(int dtype, const Moe &m);
+hipError_t launch_moe(int dtype, const Moe &m, const Workspace &ws, hipStream_t stream);
+
+// Y = act(Z) + R elementwise over M x N in fp32, in place where Y is Z.
+hipError_t launch_finish32(int M, int N, const float *Z, long long ldz, int act, const float *R,
+                           long long ldr, float *Y, long long ldy, hipStream_t stream);
+
+// Whether rows of an array take 16-byte accesses.
+inline bool rows16(const void *q, long long ld, int elem) {
+    return reinterpret_cast<unsigned long long>(q) % 16 == 0 && ld * elem % 16 == 0;
+}
+inline int epilogue_vec(const Prod &p, int elem) {
+    return rows16(p.C, p.ldc, elem) && (!p.R || rows16(p.R, p.ldr, elem)) &&
+           (!p.Z || rows16(p.Z, p.ldz, elem)) && (!p.bias || rows16(p.bias, 16, elem));
+}
+
+// ---- device helpers ---------------------------------------------------------
+
+// Slope of an activation at its input (SGEMM_ACT_*), in fp32.  ReLU's slope at
+// 0 is 0.
+template <int ACT>
+__device__ __forceinline__ float slope_t(float x) {
+    if constexpr (ACT == SGEMM_ACT_RELU) {
+        return x > 0.f ? 1.f : (x <= 0.f ? 0.f : x);   // NaN stays NaN
+    } else if constexpr (ACT == SGEMM_ACT_SILU) {
+        // s (1 + x (1 - s)) with 1 - s = sigmoid(-x), which keeps its digits
+        // where s rounds to 1; x (1 - s) -> 0 for x -> inf through e^-x
+        const float e = expf(-fabsf(x));
+        const float r = 1.f / (1.f + e);
+        const float s = x >= 0.f ? r : e * r, c = x >= 0.f ? e * r : r;
+        return x == -INFINITY || x == INFINITY ? s : s * (1.f + x * c);
+    } else if constexpr (ACT == SGEMM_ACT_GELU_ERF) {
+        const float phi = 0.39894228040143268f * expf(-0.5f * x * x);
+        return 0.5f * erfcf(-0.70710678118654752f * x) +
+               (fabsf(x) == INFINITY ? 0.f : x * phi);
+    } else if constexpr (ACT == SGEMM_ACT_GELU_TANH) {
+        // q = (1 + tanh u) / 2 = sigmoid(2u): slope q + 2 x q (1 - q) u'
+        const float x2 = x * x;
+        const float u = 0.79788456080286536f * fmaf(0.044715f * x, x2, x);
+        const float du = 0.79788456080286536f * fmaf(0.134145f, x2, 1.f);
+        const float e = expf(-2.f * fabsf(u));
+        const float r = 1.f / (1.f + e);
+        const float q = u >= 0.f ? r : e * r;
+        // e r^2 = q (1 - q); it is 0 in fp32 long before x du overflows
+        const float t = e * r * r;
+        return t == 0.f ? q : q + 2.f * x * t * du;
+    } else {
+        return 1.f;
+    }
+}
+
+// 16-bit values to and from fp32 (round to nearest, ties to even).
+template <int DT>
+__device__ __forceinline__ float widen(u16 v) {
+    if constexpr (DT == SGEMM_DTYPE_BF16)
+        return __builtin_bit_cast(float, (unsigned)v << 16);
+    else
+        return (float)__builtin_bit_cast(_Float16, v);
+}
+template <int DT>
+__device__ __forceinline__ u16 narrow(float v) {
+    if constexpr (DT == SGEMM_DTYPE_BF16)
+        return __builtin_bit_cast(u16, (__bf16)v);
+    else
+        return __builtin_bit_cast(u16, (_Float16)v);
+}
+
+// Values of one type as the kernels load and store them, V to 16 bytes.
+template <int DT>
+struct Type {
+    using T = u16;
+    static constexpr int V = 8;
+    static __device__ __forceinline__ float load(T v) { return widen<DT>(v); }
+    static __device__ __forceinline__ T store(float v) { return narrow<DT>(v); }
+};
+template <>
+struct Type<SGEMM_DTYPE_F32> {
+    using T = float;
+    static constexpr int V = 4;
+    static __device__ __forceinline__ float load(T v) { return v; }
+    static __device__ __forceinline__ T store(float v) { return v; }
+};
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef unsigned uintx4 __attribute__((ext_vector_type(4)));
+typedef unsigned uintx2 __attribute__((ext_vector_type(2)));
+
+// D += A B over 32 k values of 16-bit inputs.  Lane (i, g) = (lane % 16,
+// lane / 16): a holds A(row i, k = 8g .. 8g+7), b holds B(column i, same k),
+// and c holds D(rows 4g .. 4g+3, column i).
+template <int DT>
+__device__ __forceinline__ floatx4 mfma16(uintx4 a, uintx4 b, floatx4 c) {
+    if constexpr (DT == SGEMM_DTYPE_BF16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                       __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a),
+                                                      __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
+}
+
+// Calls f with the activation code as a compile-time constant.
+template <class F>
+__device__ __forceinline__ void with_act(int act, F &&f) {
+    switch (act) {
+    case SGEMM_ACT_RELU: f(std::integral_constant<int, SGEMM_ACT_RELU>{}); break;
+    case SGEMM_ACT_SILU: f(std::integral_constant<int, SGEMM_ACT_SILU>{}); break;
+    case SGEMM_ACT_GELU_ERF: f(std::integral_constant<int, SGEMM_ACT_GELU_ERF>{}); break;
+    case SGEMM_ACT_GELU_TANH: f(std::integral_constant<int, SGEMM_ACT_GELU_TANH>{}); break;
+    default: f(std::integral_constant<int, SGEMM_ACT_NONE>{}); break;
+    }
+}
+
+// Bias, activation, residual and the store of the CN adjacent columns from n
+// on (n a multiple of 4, of 8 where CN >= 8) of row m < p.M.  R may be C: each
+// cell is read before it is written, by the same lane.
+template <int DT, int ACT, int CN>
+__device__ __forceinline__ void finish_run(const Prod &p, int m, int n, const float (&v)[CN]) {
+    using Ty = Type<DT>;
+    using T = typename Ty::T;
+    constexpr int W = CN < Ty::V ? CN : Ty::V;   // values per access
+    constexpr int BYTES = W * sizeof(T);
+    static_assert(CN % W == 0, "whole accesses");
+    T *c = static_cast<T *>(p.C) + (long long)m * p.ldc;
+    const T *r = p.R ? static_cast<const T *>(p.R) + (long long)m * p.ldr : nullptr;
+    T *z = p.Z ? static_cast<T *>(p.Z) + (long long)m * p.ldz : nullptr;
+    const T *bias = static_cast<const T *>(p.bias);
+#pragma unroll
+    for (int h = 0; h < CN; h += W) {
+        const int n1 = n + h;
+        if (n1 >= p.N) return;
+        if (p.cvec && n1 + W <= p.N) {
+            T t[W];
+            float x[W], res[W];
+            if (r) {
+                __builtin_memcpy(t, __builtin_assume_aligned(r + n1, BYTES), BYTES);
+#pragma unroll
+                for (int e = 0; e < W; ++e) res[e] = Ty::load(t[e]);
+            }
+            if (bias) {
+                __builtin_memcpy(t, __builtin_assume_aligned(bias + n1, BYTES), BYTES);
+#pragma unroll
+                for (int e = 0; e < W; ++e) x[e] = v[h + e] + Ty::load(t[e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < W; ++e) x[e] = v[h + e];
+            }
+            if (z) {
+#pragma unroll
+                for (int e = 0; e < W; ++e) t[e] = Ty::store(x[e]);
+                __builtin_memcpy(__builtin_assume_aligned(z + n1, BYTES), t, BYTES);
+            }
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                const float y = activate_t<ACT>(x[e]);
+                t[e] = Ty::store(r ? y + res[e] : y);
+            }
+            __builtin_memcpy(__builtin_assume_aligned(c + n1, BYTES), t, BYTES);
+        } else {
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                if (n1 + e >= p.N) continue;
+                const float s = bias ? v[h + e] + Ty::load(bias[n1 + e]) : v[h + e];
+                if (z) z[n1 + e] = Ty::store(s);
+                const float y = activate_t<ACT>(s);
+                c[n1 + e] = Ty::store(r ? y + Ty::load(r[n1 + e]) : y);
+            }
+        }
+    }
+}
+
+// Partial sums that another workgroup adds up are stored and loaded as
+// device-coherent accesses, which bypass the per-XCD caches (these are not
+// coherent with each other); a workgroup counts its arrival after every wave
+// has waited for its stores.
+__device__ __forceinline__ void store_partial(float *d, const floatx4 &v) {
+    const float f[4] = {v[0], v[1], v[2], v[3]};
+    unsigned long long w[2];
+    __builtin_memcpy(w, f, 16);
+    unsigned long long *q = reinterpret_cast<unsigned long long *>(d);
+    __hip_atomic_store(q, w[0], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store(q + 1, w[1], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ floatx4 load_partial(const float *d) {
+    const unsigned long long *q = reinterpret_cast<const unsigned long long *>(d);
+    unsigned long long w[2];
+    w[0] = __hip_atomic_load(q, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    w[1] = __hip_atomic_load(q + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    float f[4];
+    __builtin_memcpy(f, w, 16);
+    return floatx4{f[0], f[1], f[2], f[3]};
+}
+
+// Counts this workgroup's arrival at *count and returns, to every thread,
+// whether it is the last of n.  `flag`: one int of LDS.
+__device__ __forceinline__ bool arrive_last(unsigned *count, unsigned n, int *flag) {
+    __builtin_amdgcn_s_waitcnt(0);   // this wave's partial sums are in memory
+    __syncthreads();
+    if (threadIdx.x == 0)
+        *flag = __hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                n - 1;
+    __syncthreads();
+    return *flag != 0;
+}
+
+}  // namespace sg

@@ -60,7 +60,7 @@ struct Cached {
     size_t bytes = 0;      // bytes for the sums
 };
 
-using Key = std::tuple<int, hipStream_t, std::thread::id>;
+using Key = std::tuple<int, hipStream_t, std::thread::id, int>;
 
 std::mutex &cache_mutex() {
     static std::mutex m;
@@ -102,7 +102,8 @@ hipError_t static_scratch(void **ptr, size_t *bytes) {
     return hipSuccess;
 }
 
-hipError_t workspace_acquire(size_t bytes, hipStream_t stream, const Problem &p, Workspace &w) {
+hipError_t workspace_acquire(size_t bytes, hipStream_t stream, const Problem &p, Workspace &w,
+                             int kind) {
     w = Workspace{};
     if (p.scratch) {
         // the caller's scratch (checked against the plan before any launch)
@@ -126,7 +127,7 @@ hipError_t workspace_acquire(size_t bytes, hipStream_t stream, const Problem &p,
     const std::thread::id tid =
         stream == hipStreamPerThread ? std::this_thread::get_id() : std::thread::id();
     std::lock_guard<std::mutex> lock(cache_mutex());
-    Cached &c = cache()[Key{dev, stream, tid}];
+    Cached &c = cache()[Key{dev, stream, tid, kind}];
     if (c.bytes < bytes || !c.ptr) {
         if (c.ptr) {
             e = hipFreeAsync(c.ptr, stream);

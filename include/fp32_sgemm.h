@@ -69,6 +69,8 @@
  *     -30               sgemm_mixed: dtype not SGEMM_DTYPE_BF16 / _F16
  *     -31               sgemm_op_ex_noalloc: the plan's partial sums need
  *                       more memory than the static scratch holds
+ *     -(100 + i)        sgemm_linear, sgemm_linear_backward, sgemm_moe: the
+ *                       i-th argument is invalid (1-based)
  *     > 0               a hipError_t reported by the kernel launch
  * No C++ exception crosses this interface.
  *
@@ -103,6 +105,9 @@ enum sgemm_variant {
 /* Input formats of sgemm_mixed. */
 #define SGEMM_DTYPE_BF16 1   /* bfloat16: the high 16 bits of an IEEE binary32 */
 #define SGEMM_DTYPE_F16 2    /* IEEE binary16 */
+
+/* ... and of the feed-forward operators, which take fp32 as well. */
+#define SGEMM_DTYPE_F32 0    /* IEEE binary32 */
 
 /* sgemm_config.flags bits */
 #define SGEMM_FLAG_SCALAR_IO 0x1   /* force 4-byte loads/stores (no 16-byte vectors) */
@@ -395,6 +400,81 @@ int sgemm_version(void);
  * may receive the same handle value and would otherwise inherit the buffer.
  */
 int sgemm_workspace_release(void);
+
+/*
+ * The feed-forward operators.  Every array of a call has one type, dtype
+ * (SGEMM_DTYPE_F32, _BF16 or _F16); sums, activations and the residual are
+ * computed in fp32 and each result is rounded once.  Arrays are row-major with
+ * leading dimensions in elements, aligned to their type's size, rows of any
+ * alignment beyond that (16-byte rows run fastest).  Padding is neither read
+ * nor written.  An argument that is not given is NULL and its leading
+ * dimension then ignored.  Results must not overlap inputs or one another,
+ * but for sgemm_linear's Y, which may be R itself with the same leading
+ * dimension (the residual is then added in place).  Status -(100 + i) names
+ * the i-th argument.
+ *
+ * Intermediate values live in a workspace of their own per device and stream
+ * (per host thread for the per-thread default stream), grown when a call needs
+ * more and released by sgemm_workspace_release: an M x N array for a backward
+ * pass with an activation and for the fp32 linear layer with a residual of
+ * more than 64 rows; partial sums of products split over their inner length;
+ * for the experts T * top_k * (F + D) values.  Under graph capture it is the
+ * graph's own, as for the products.  The launches of a call are made together:
+ * host threads that share a stream do not interleave them.
+ */
+
+/*
+ * sgemm_linear: Y = act(X W^T + bias) + R, a linear layer with its whole
+ * epilogue.  dtype; M, N, K >= 0; X (M x K, ldx); W (N x K, ldw); bias (N
+ * values, or NULL); R (M x N, ldr, or NULL); act (SGEMM_ACT_*); Y (M x N,
+ * ldy); Z (M x N, ldz, or NULL): receives X W^T + bias, the activation's
+ * input, which the backward pass takes; stream.  Y is computed from the
+ * unrounded sum, not from Z.  M == 0 or N == 0: nothing is done; K == 0: the
+ * product is zero and X and W are not read.
+ */
+int sgemm_linear(int dtype, int M, int N, int K, const void *X, int ldx, const void *W, int ldw,
+                 const void *bias, const void *R, int ldr, int act, void *Y, int ldy, void *Z,
+                 int ldz, hipStream_t stream);
+
+/*
+ * sgemm_linear_backward: the gradients of sgemm_linear for a gradient dY of
+ * its result: with G = dY * act'(Z),
+ *     dX = G W,  dW = G^T X,  db = the sum of G's rows.
+ * (The gradient of R is dY itself.)  dtype; M, N, K >= 0; dY (M x N, lddy);
+ * Z (M x N, ldz; not read when act is SGEMM_ACT_NONE, and may then be NULL);
+ * act; X (M x K, ldx; read for dW); W (N x K, ldw; read for dX); dX (M x K,
+ * lddx), dW (N x K, lddw), db (N values): each may be NULL and is then not
+ * computed; stream.  ReLU's slope at 0 is 0.  db is summed from the unrounded
+ * G in fp32.  For 16-bit types with an activation and more than 64 rows, G is
+ * rounded to dtype for the two products; with fewer it is held in two parts.
+ * Empty sums are written as zeros (dW and db when M == 0, dX when N == 0).
+ */
+int sgemm_linear_backward(int dtype, int M, int N, int K, const void *dY, int lddy, const void *Z,
+                          int ldz, int act, const void *X, int ldx, const void *W, int ldw,
+                          void *dX, int lddx, void *dW, int lddw, void *db, hipStream_t stream);
+
+/*
+ * sgemm_moe: a whole mixture-of-experts layer for a few tokens.
+ *     logits = X Wr^T,  p = softmax(logits) over the E experts,
+ *     e_1 .. e_k: the k largest logits (equal ones: the lowest index),
+ *     w_j = p[e_j], divided by the sum of the k when renormalize is 1,
+ *     h_j = act(W1[e_j] x)                          gated == 0
+ *     h_j = act(W1[e_j][0 .. F-1] x) * (W1[e_j][F .. 2F-1] x)   gated == 1
+ *     Y   = sum_j w_j W2[e_j] h_j.
+ * dtype; T (tokens, 0 .. 64); D (1 .. 64512); F (1 .. 2^20); E (1 .. 512);
+ * top_k (1 .. min(E, 16)); gated; renormalize; act; X (T x D, ldx); Wr (E x D,
+ * ldr); W1 (E matrices of F or 2F rows of D, ld1, stride1 elements apart); W2
+ * (E matrices of D rows of F, ld2, stride2 apart); Y (T x D, ldy); ids (T x
+ * top_k ints, or NULL): receives the chosen experts in order; weights (T x
+ * top_k floats, or NULL): receives w; stream.  The logits are summed in fp64.
+ * h is held in fp32 (fp32 inputs) or as the sum of two values of dtype (a
+ * float16 h beyond 65504 is infinite).  A NaN logit ranks lowest and makes
+ * all weights of its token NaN.  Other tokens' results do not depend on it.
+ */
+int sgemm_moe(int dtype, int T, int D, int F, int E, int top_k, int gated, int renormalize, int act,
+              const void *X, int ldx, const void *Wr, int ldr, const void *W1, int ld1,
+              long long stride1, const void *W2, int ld2, long long stride2, void *Y, int ldy,
+              int *ids, float *weights, hipStream_t stream);
 
 #ifdef __cplusplus
 }

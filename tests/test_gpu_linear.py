@@ -1,0 +1,252 @@
+"""Linear layers with their whole epilogue, and their backward pass, against the
+definition in 64 bits; integer-valued inputs bit for bit."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import fp32_sgemm_02_amd as sg
+from tests import linear_ref as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+TYPES = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+
+
+def view(rows, cols, dtype, pad, off, gen, ints=False, scale=1.0):
+    """A rows x cols view with `pad` extra values a row and `off` values before
+    the first, all of those NaN."""
+    buf = torch.full((rows * (cols + pad) + off + 8,), float("nan"), device=DEV, dtype=dtype)
+    v = buf[off:off + rows * (cols + pad)].view(rows, cols + pad)[:, :cols]
+    if ints:
+        v.copy_(torch.randint(-3, 4, (rows, cols), generator=gen, device=DEV).to(dtype))
+    else:
+        v.copy_((torch.randn(rows, cols, generator=gen, device=DEV) * scale).to(dtype))
+    return v, buf
+
+
+def gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def untouched(v, buf):
+    """The values of buf outside its view v are still NaN."""
+    mask = torch.ones_like(buf, dtype=torch.bool)
+    o = v.storage_offset()
+    mask.as_strided(v.shape, v.stride(), o)[...] = False
+    return bool(torch.isnan(buf[mask]).all())
+
+
+# one token to many tiles; odd sizes; edges inside chunks, stages and tiles
+SHAPES = [
+    (1, 1, 1), (1, 17, 5), (2, 64, 64), (1, 4096, 512), (3, 100, 129), (15, 33, 257),
+    (16, 256, 1024), (17, 130, 96), (33, 64, 200), (48, 1000, 72), (64, 48, 4096),
+    (65, 65, 65), (100, 1, 300), (65, 3000, 8), (128, 128, 128), (130, 257, 1000), (200, 136, 2049),
+    (515, 264, 136), (300, 1111, 640), (1025, 2047, 72), (2048, 2176, 136),
+]
+
+
+@pytest.mark.parametrize("t", list(TYPES))
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_linear_integers_bit_exact(M, N, K, t):
+    """Integer inputs: every sum is exact in 32 bits, so the result is the exact
+    value rounded once.  Padded rows hold NaN and stay as they were."""
+    dt, g = TYPES[t], gen(M * 7 + N * 3 + K)
+    for n, (pad, off, name) in enumerate([(0, 0, "none"), (8, 0, "relu"), (3, 1, "relu")]):
+        X, _ = view(M, K, dt, pad, off, g, True)
+        W, _ = view(N, K, dt, pad, off, g, True)
+        b, _ = view(1, N, dt, 0, off, g, True)
+        R, _ = view(M, N, dt, pad, off, g, True)
+        out, obuf = view(M, N, dt, pad, off, g, True)
+        pre, pbuf = view(M, N, dt, pad, off, g, True)
+        out.fill_(float("nan"))
+        b, R = (None, None) if n == 1 else (b[0], R)
+        Y, Z = sg.linear(X, W, b, act=ref.ACTS[name], residual=R, keep_pre=True, out=out, pre=pre)
+        y, z, _ = ref.linear(X, W, b, R, name)
+        assert torch.equal(Z, z.to(dt)), (pad, off)
+        assert torch.equal(Y, y.to(dt)), (pad, off)
+        assert Y.data_ptr() == out.data_ptr()
+        assert untouched(out, obuf) and untouched(pre, pbuf)
+
+
+@pytest.mark.parametrize("t", list(TYPES))
+@pytest.mark.parametrize("name", list(ref.ACTS))
+@pytest.mark.parametrize("M,N,K", [(1, 300, 257), (16, 512, 768), (40, 100, 1000), (150, 200, 264),
+                                   (700, 400, 333), (1100, 2304, 512)])
+def test_linear_random(M, N, K, name, t):
+    dt, g = TYPES[t], gen(M + N + K)
+    X, _ = view(M, K, dt, 0, 0, g)
+    W, _ = view(N, K, dt, 0, 0, g, scale=K ** -0.5)
+    b, _ = view(1, N, dt, 0, 0, g)
+    R, _ = view(M, N, dt, 0, 0, g)
+    for bias, res in ((None, None), (b[0], R)):
+        Y, Z = sg.linear(X, W, bias, act=ref.ACTS[name], residual=res, keep_pre=True)
+        y, z, zb = ref.linear(X, W, bias, res, name)
+        assert bool(((Z.double() - z).abs() <= zb + ref.rounding(z.abs() + zb, dt)).all())
+        assert bool(((Y.double() - y).abs() <= ref.linear_bound(y, z, zb, res, name, dt)).all())
+
+
+@pytest.mark.parametrize("t", list(TYPES))
+@pytest.mark.parametrize("M", [1, 20, 70, 300])
+def test_linear_residual_in_place(M, t):
+    dt, g = TYPES[t], gen(M)
+    X, W, R = (view(r, c, dt, 0, 0, g, True)[0] for r, c in ((M, 128), (264, 128), (M, 264)))
+    y, _, _ = ref.linear(X, W, None, R, "relu")
+    sg.linear(X, W, act=sg.ACT_RELU, residual=R, out=R)
+    assert torch.equal(R, y.to(dt))
+
+
+@pytest.mark.parametrize("t", list(TYPES))
+@pytest.mark.parametrize("M", [1, 70])
+def test_linear_empty_inner(M, t):
+    """K == 0: the activation of the bias, plus the residual."""
+    dt, g = TYPES[t], gen(1)
+    b, R = view(1, 40, dt, 0, 0, g, True)[0][0], view(M, 40, dt, 0, 0, g, True)[0]
+    X, W = torch.empty(M, 0, device=DEV, dtype=dt), torch.empty(40, 0, device=DEV, dtype=dt)
+    assert torch.equal(sg.linear(X, W, b, act=sg.ACT_RELU, residual=R),
+                       (b.double().clamp_min(0) + R.double()).to(dt))
+    assert sg.linear(torch.empty(0, 8, device=DEV, dtype=dt),
+                     torch.empty(40, 8, device=DEV, dtype=dt)).shape == (0, 40)
+
+
+def test_linear_extreme_values():
+    """Infinities and NaN travel through their own rows and columns only."""
+    for t, dt in TYPES.items():
+        for M in (3, 70):
+            g = gen(5)
+            X, _ = view(M, 96, dt, 0, 0, g)
+            W, _ = view(40, 96, dt, 0, 0, g)
+            X[1, 3] = float("nan")
+            X[2, 4] = float("inf")
+            Y = sg.linear(X, W)
+            keep = [m for m in range(M) if m not in (1, 2)]
+            assert bool(torch.isnan(Y[1]).all())
+            assert not bool(torch.isfinite(Y[2]).any())
+            y, z, zb = ref.linear(X[keep], W, None, None, "none")
+            assert bool(((Y[keep].double() - y).abs()
+                         <= ref.linear_bound(y, z, zb, None, "none", dt)).all())
+            for name, code in ref.ACTS.items():
+                b = torch.tensor([float("inf"), float("-inf"), 88.0, -88.0] * 10, device=DEV).to(dt)
+                Y = sg.linear(torch.zeros_like(X), W, b, act=code)
+                want = ref.act(name, b.double())
+                if name != "none":   # act(-inf) is 0 (the limit)
+                    want = torch.where(torch.isneginf(b), torch.zeros_like(want), want)
+                    got = torch.where(torch.isneginf(b), torch.zeros_like(Y), Y)
+                else:
+                    got = Y
+                assert bool((got[0].double() == want.to(dt).double()).all()) or \
+                    bool(((got[0].double() - want).abs() <= ref.rounding(want, dt) +
+                          8 * ref.U32 * want.abs())[torch.isfinite(want)].all()), (t, name)
+
+
+@pytest.mark.parametrize("t", list(TYPES))
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_backward_integers_bit_exact(M, N, K, t):
+    dt, g = TYPES[t], gen(M + 5 * N + K)
+    for pad, off, name in [(0, 0, "none"), (8, 0, "relu"), (3, 1, "relu"), (5, 3, "none")]:
+        X, _ = view(M, K, dt, pad, off, g, True)
+        W, _ = view(N, K, dt, pad, off, g, True)
+        dY, _ = view(M, N, dt, pad, off, g, True)
+        Z, _ = view(M, N, dt, pad, off, g, True)
+        got = sg.linear_backward(dY, X, W, Z, act=ref.ACTS[name])
+        want = ref.backward(dY, X, W, Z, name)
+        for n, (a, b) in enumerate(zip(got, want)):
+            assert torch.equal(a, b.to(dt)), (n, pad, off)
+
+
+@pytest.mark.parametrize("t", list(TYPES))
+@pytest.mark.parametrize("name", list(ref.ACTS))
+@pytest.mark.parametrize("M,N,K", [(1, 300, 257), (16, 512, 768), (40, 100, 1000), (64, 264, 64),
+                                   (150, 200, 264), (700, 400, 333), (2100, 640, 512)])
+def test_backward_random(M, N, K, name, t):
+    dt, g = TYPES[t], gen(M + N + K)
+    X, _ = view(M, K, dt, 0, 0, g)
+    W, _ = view(N, K, dt, 0, 0, g, scale=K ** -0.5)
+    dY, _ = view(M, N, dt, 0, 0, g)
+    Z, _ = view(M, N, dt, 0, 0, g, scale=2.0)
+    dX, dW, db = sg.linear_backward(dY, X, W, Z, act=ref.ACTS[name])
+    rx, rw, rb, G = ref.backward(dY, X, W, Z, name)
+    e = ref.grad_bound(G, dY, name, dt, M <= 64)
+    e32 = ref.grad_bound(G, dY, name, torch.float32, False)
+    a = G.abs() + e
+    for got, want, bound in (
+            (dX, rx, e @ W.double().abs() + 2 * N * ref.U32 * (a @ W.double().abs())),
+            (dW, rw, e.t() @ X.double().abs() + 2 * M * ref.U32 * (a.t() @ X.double().abs())),
+            (db, rb, e32.sum(0) + M * ref.U32 * (G.abs() + e32).sum(0))):
+        assert bool(((got.double() - want).abs()
+                     <= bound + ref.rounding(want.abs() + bound, dt)).all())
+
+
+@pytest.mark.parametrize("name", list(ref.ACTS))
+def test_backward_against_differences(name):
+    """fp32 gradients against central differences of the 64-bit definition: with
+    step h the difference is off by h^2 / 6 of a third derivative (below 4 for
+    each activation, times the weights' cubes) plus the 64-bit rounding."""
+    g = gen(11)
+    M, N, K = 5, 12, 9
+    X, W, dY = (torch.randn(r, c, generator=g, device=DEV).double() for r, c in ((M, K), (N, K), (M, N)))
+    X, W, dY = (v.float() for v in (X, W, dY))
+    b = torch.randn(N, generator=g, device=DEV)
+    _, Z = sg.linear(X, W, b, act=ref.ACTS[name], keep_pre=True)
+    dX, dW, db = sg.linear_backward(dY, X, W, Z, act=ref.ACTS[name])
+
+    def loss(x, w, c):
+        return float((ref.act(name, x @ w.t() + c) * dY.double()).sum())
+
+    h = 1e-4
+    x0, w0, b0 = X.double(), W.double(), b.double()
+    for t, grad in ((x0, dX), (w0, dW), (b0, db)):
+        flat = t.view(-1)
+        for i in range(0, flat.numel(), 5):
+            v = float(flat[i])
+            flat[i] = v + h
+            up = loss(x0, w0, b0)
+            flat[i] = v - h
+            down = loss(x0, w0, b0)
+            flat[i] = v
+            want = (up - down) / (2 * h)
+            cubes = float(dY.abs().max()) * max(M, N) * 4 * max(
+                1.0, float(x0.abs().max()), float(w0.abs().max())) ** 3
+            bound = h * h / 6 * cubes + 200 * ref.U32 * float(dY.abs().sum()) * 4
+            assert abs(float(grad.view(-1)[i]) - want) <= bound
+
+
+@pytest.mark.parametrize("t", list(TYPES))
+def test_backward_parts_and_empty(t):
+    dt, g = TYPES[t], gen(2)
+    for M in (6, 80):
+        X, W, dY, Z = (view(r, c, dt, 0, 0, g, True)[0]
+                       for r, c in ((M, 24), (40, 24), (M, 40), (M, 40)))
+        full = sg.linear_backward(dY, X, W, Z, act=sg.ACT_RELU)
+        for need in ((1, 0, 0), (0, 1, 0), (0, 0, 1), (0, 0, 0)):
+            part = sg.linear_backward(dY, X, W, Z, act=sg.ACT_RELU, need_x=need[0],
+                                      need_w=need[1], need_bias=need[2])
+            for n in range(3):
+                assert (part[n] is None) == (not need[n])
+                assert part[n] is None or torch.equal(part[n], full[n])
+    e = lambda *s: torch.empty(*s, device=DEV, dtype=dt)
+    for act in (sg.ACT_NONE, sg.ACT_SILU):
+        dX, dW, db = sg.linear_backward(e(0, 40), e(0, 24), e(40, 24), e(0, 40), act=act)
+        assert dX.shape == (0, 24) and not dW.any() and not db.any()
+        for M in (5, 80):
+            dX, dW, db = sg.linear_backward(e(M, 0), e(M, 24), e(0, 24), e(M, 0), act=act)
+            assert not dX.any() and dW.shape == (0, 24) and db.shape == (0,)
+            dX, dW, db = sg.linear_backward(torch.ones(M, 40, device=DEV, dtype=dt), e(M, 0), e(40, 0),
+                                            torch.ones(M, 40, device=DEV, dtype=dt),
+                                            act=sg.ACT_RELU if act else act)
+            assert dX.shape == (M, 0) and bool((db == M).all())
+
+
+@pytest.mark.parametrize("t", list(TYPES))
+def test_repeatable(t):
+    """Split sums are added in a fixed order: bitwise equal results, call after
+    call."""
+    dt, g = TYPES[t], gen(3)
+    for M, N, K in ((1, 128, 4096), (16, 64, 8192), (100, 100, 6000), (300, 200, 3000)):
+        X, W, dY, Z = (view(r, c, dt, 0, 0, g)[0] for r, c in ((M, K), (N, K), (M, N), (M, N)))
+        Y = sg.linear(X, W)
+        G = sg.linear_backward(dY, X, W, Z, act=sg.ACT_SILU)
+        for _ in range(3):
+            assert torch.equal(sg.linear(X, W), Y)
+            for a, b in zip(sg.linear_backward(dY, X, W, Z, act=sg.ACT_SILU), G):
+                assert torch.equal(a, b)
