@@ -28,7 +28,7 @@ ARCH = "gfx950"
 SOURCES = ["api.cpp", "workspace.cpp", "scale.hip", "mfma_gemm.hip", "mfma_direct.hip", "mfma_direct_epi.hip",
            "mfma_direct_sk.hip",
            "mfma_direct_ta.hip", "mfma_direct_ta_epi.hip", "mfma_gemm16.hip", "valu_gemm.hip",
-           "skinny_gemm.hip", "small_gemm.hip", "linear.cpp", "linear16.hip", "linear_rows.hip",
+           "skinny_gemm.hip", "small_gemm.hip", "linear.cpp", "linear16.hip", "linear16_big.hip", "linear_rows.hip",
            "linear_grad.hip", "moe.hip"]
 PROBE_SOURCES = ["peak_probes.hip"]
 PROBE_LIB = os.path.join(HERE, "libfp32probes.so")

@@ -292,18 +292,22 @@ bool direct_ok(const void *q, long long ld, int row_len, int bt, int mc) {
 
 struct Plan16 {
     int bm, bn, slices, per;
+    bool big;   // linear16_big.hip
 };
 
 constexpr int kCUs = 256;
 
 Plan16 plan16(const Prod &p) {
     auto tiles = [&](int b) { return (long long)((p.M + b - 1) / b) * ((p.N + b - 1) / b); };
-    Plan16 q;
+    Plan16 q{};
+    q.big = !p.fold && tiles(256) >= kCUs / 2 &&
+            direct_ok(p.A, p.lda, p.a_pad ? 0 : p.a_mc ? p.M : p.K, 256, p.a_mc) &&
+            direct_ok(p.B, p.ldb, p.b_mc ? p.N : p.K, 256, p.b_mc);
     q.bm = q.bn = tiles(128) >= kCUs ? 128 : 64;
     const long long t = tiles(q.bm);
     const int stages = p.fold ? 2 : (p.K + kBK - 1) / kBK;
     int s = 1;
-    if (!p.fold && t < 2 * kCUs && t <= kWorkspaceCounters) {
+    if (!p.fold && !q.big && t < 2 * kCUs && t <= kWorkspaceCounters) {
         s = (int)((2 * kCUs + t - 1) / t);
         const int most = stages / 4;
         if (s > most) s = most;
@@ -343,6 +347,7 @@ template <int DT>
 hipError_t launch_dt(Prod p, const Workspace &ws, hipStream_t stream) {
     const Plan16 q = plan16(p);
     p.cvec = epilogue_vec(p, 2);
+    if (q.big) return launch_prod16_big(DT, p, stream);
     Grid16 gr{};
     gr.tiles_m = (p.M + q.bm - 1) / q.bm;
     gr.tiles_n = (p.N + q.bn - 1) / q.bn;

@@ -48,6 +48,10 @@ struct Prod {
 size_t prod16_workspace(int dtype, const Prod &p);
 hipError_t launch_prod16(int dtype, const Prod &p, const Workspace &ws, hipStream_t stream);
 
+// The tile kernel of large products (linear16_big.hip), for operands whose
+// rows take direct 16-byte loads.
+hipError_t launch_prod16_big(int dtype, const Prod &p, hipStream_t stream);
+
 // Few-rows kernels (linear_rows.hip), M <= kFewRows, every type, A with k
 // contiguous and either B: B is streamed once, from memory into registers.
 constexpr int kFewRows = 64;

@@ -43,6 +43,8 @@ SHAPES = [
     (16, 256, 1024), (17, 130, 96), (33, 64, 200), (48, 1000, 72), (64, 48, 4096),
     (65, 65, 65), (100, 1, 300), (65, 3000, 8), (128, 128, 128), (130, 257, 1000), (200, 136, 2049),
     (515, 264, 136), (300, 1111, 640), (1025, 2047, 72), (2048, 2176, 136),
+    # 128 tiles of 256 x 256 and more, for each of the three products; one to four stages
+    (4100, 2184, 136), (4104, 136, 2184), (200, 4104, 2184), (2568, 3336, 8),
 ]
 
 
