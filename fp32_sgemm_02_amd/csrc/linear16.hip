@@ -35,9 +35,11 @@ typedef s16x4 __attribute__((address_space(3))) lds_s16x4;
 constexpr int kBK = 64;                            // k per stage
 constexpr int kOutOfRange = (int)0x80000000u;      // a buffer offset that reads zero
 
+// Waits for this wave's LDS accesses and for all but its last N vector loads.
 template <int N>
-__device__ __forceinline__ void wait_vmcnt() {
-    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+__device__ __forceinline__ void wait_loads() {
+    pipeline_fence();
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
 }
 
 // Tile row held in image row r, groups of G 16-row blocks.
@@ -176,14 +178,13 @@ struct Grid16 {
 // finishes the tile (its acc then holds the whole sum).
 template <int NB, int MB, int NT>
 __device__ __forceinline__ bool join_slices(const Grid16 &gr, int tile, int tiles, int slice,
-                                            int tid, floatx4 (&acc)[NB][MB]) {
-    __shared__ int last;
+                                            int tid, int *last, floatx4 (&acc)[NB][MB]) {
     auto at = [&](int s, int j) {
         return gr.part + ((((long long)s * tiles + tile) * (NB * MB) + j) * NT + tid) * 4;
     };
 #pragma unroll
     for (int j = 0; j < NB * MB; ++j) store_partial(at(slice, j), acc[j / MB][j % MB]);
-    if (!arrive_last(gr.count + tile, gr.slices, &last)) return false;
+    if (!arrive_last(gr.count + tile, gr.slices, last)) return false;
 #pragma unroll
     for (int j = 0; j < NB * MB; ++j) acc[j / MB][j % MB] = load_partial(at(0, j));
     for (int s = 1; s < gr.slices; ++s)
@@ -197,10 +198,13 @@ __device__ __forceinline__ bool join_slices(const Grid16 &gr, int tile, int tile
     return true;
 }
 
-// The tile kernel: BM x BN of C per workgroup, WM x WN per wave, two stages in
-// LDS, one barrier per stage.
-template <int DT, int BM, int BN, int WM, int WN, int AMC, int BMC, bool ADIR, bool BDIR>
-__global__ void __launch_bounds__(64 * (BM / WM) * (BN / WN))
+// The tile kernel: BM x BN of C per workgroup, WM x WN per wave, NBUF stages in
+// LDS, one barrier per stage.  With direct loads NBUF - 1 stages are in flight
+// (those past the end read zeros, which touch no memory and keep the count of
+// outstanding loads); operands that pass through registers have two.
+template <int DT, int BM, int BN, int WM, int WN, int NBUF_, int AMC, int BMC, bool ADIR, bool BDIR>
+__global__ void __launch_bounds__(512)   // at most 256 registers a lane: with more the compiler
+                                         // keeps moving the accumulators between register files
 prod16_kernel(Prod p, Grid16 gr) {
 #ifdef __HIP_DEVICE_COMPILE__   // the host pass needs the launch stub only
     constexpr int WAVES_N = BN / WN, NW = (BM / WM) * WAVES_N, NT = 64 * NW;
@@ -208,7 +212,9 @@ prod16_kernel(Prod p, Grid16 gr) {
     constexpr int GM = MB < 4 ? MB : 4, GN = NB < 4 ? NB : 4;
     using OpA = Operand<BM, AMC, ADIR, GM, NW>;
     using OpB = Operand<BN, BMC, BDIR, GN, NW>;
-    __shared__ __attribute__((aligned(1024))) unsigned char smem[2][OpA::BYTES + OpB::BYTES];
+    constexpr int NBUF = ADIR && BDIR ? NBUF_ : 2;
+    constexpr int AHEAD = NBUF - 1;   // stages in flight
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[NBUF][OpA::BYTES + OpB::BYTES];
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -234,18 +240,30 @@ prod16_kernel(Prod p, Grid16 gr) {
         for (int x = 0; x < MB; ++x) acc[y][x] = floatx4{0.f, 0.f, 0.f, 0.f};
 
     auto issue = [&](int t, unsigned char *img) {
-        const int krem = p.fold ? p.K : p.K - t * kBK;
+        // stages past the slice's end read zeros
+        const int krem = t >= t1 ? 0 : p.fold ? p.K : p.K - t * kBK;
         a.issue(t, krem, img, wave);
         b.issue(p.fold ? 0 : t, krem, img + OpA::BYTES, wave);
     };
-    if (t0 < t1) issue(t0, smem[0]);
+#pragma unroll
+    for (int q = 0; q < AHEAD; ++q) issue(t0 + q, smem[q]);
+    int slot = 0;
     for (int t = t0; t < t1; ++t) {
-        unsigned char *cur = smem[(t - t0) & 1], *nxt = smem[(t - t0 + 1) & 1];
+        unsigned char *cur = smem[slot], *nxt = smem[slot == 0 ? NBUF - 1 : slot - 1];
         a.commit(cur, wave, lane);
         b.commit(cur + OpA::BYTES, wave, lane);
-        wait_vmcnt<0>();
-        __syncthreads();   // stage t is in LDS, and no wave reads the other buffer
-        if (t + 1 < t1) issue(t + 1, nxt);
+        wait_loads<(ADIR && BDIR) ? (AHEAD - 1) * (OpA::L + OpB::L) : 0>();
+        if constexpr (ADIR && BDIR) {
+            // a barrier that leaves the direct loads in flight (the reads of the
+            // stage before ended with its products)
+            pipeline_fence();
+            __builtin_amdgcn_s_barrier();
+        } else {
+            __syncthreads();
+        }
+        // stage t is in LDS, and no wave reads buffer nxt
+        pipeline_fence();
+        issue(t + AHEAD, nxt);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             uintx4 fa[MB], fb[NB];
@@ -258,26 +276,29 @@ prod16_kernel(Prod p, Grid16 gr) {
 #pragma unroll
                 for (int x = 0; x < MB; ++x) acc[y][x] = mfma16<DT>(fb[y], fa[x], acc[y][x]);
         }
+        slot = slot + 1 == NBUF ? 0 : slot + 1;
     }
-    if (gr.slices > 1 && !join_slices<NB, MB, NT>(gr, tile, tiles, slice, tid, acc)) return;
+    wait_loads<0>();   // no load of a stage past the end is left in flight
+    // (the flag of the join is in the free ring: with a second LDS object the
+    // compiler has the fragment reads wait for every direct load)
+    if (gr.slices > 1 &&
+        !join_slices<NB, MB, NT>(gr, tile, tiles, slice, tid, reinterpret_cast<int *>(smem[0]), acc))
+        return;
 
     const int i = lane & 15, g = lane >> 4;
-    with_act(p.act, [&](auto tag) {
+    with_act(p.act, [&](auto tag) __attribute__((always_inline)) {
         constexpr int ACT = decltype(tag)::value;
-#pragma unroll
-        for (int x = 0; x < MB; ++x) {
+        each<MB * (NB / GN)>([&](auto c) __attribute__((always_inline)) {
+            constexpr int x = c / (NB / GN), q = c % (NB / GN);
             const int m = m0 + wm * WM + 16 * GM * (x / GM) + 4 * GM * (i >> 2) + 4 * (x % GM) + (i & 3);
-            if (m >= p.M) continue;
+            float v[4 * GN];
 #pragma unroll
-            for (int q = 0; q < NB / GN; ++q) {
-                float v[4 * GN];
+            for (int y = 0; y < GN; ++y)
 #pragma unroll
-                for (int y = 0; y < GN; ++y)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) v[4 * y + r] = acc[q * GN + y][x][r];
+                for (int r = 0; r < 4; ++r) v[4 * y + r] = acc[q * GN + y][x][r];
+            if (m < p.M)
                 finish_run<DT, ACT>(p, m, n0 + wn * WN + 16 * GN * q + 4 * GN * g, v);
-            }
-        }
+        });
     });
 #endif
 }
@@ -320,27 +341,27 @@ Plan16 plan16(const Prod &p) {
     return q;
 }
 
-template <int DT, int BM, int BN, int WM, int WN, int AMC, int BMC>
+template <int DT, int BM, int BN, int WM, int WN, int NBUF, int AMC, int BMC>
 hipError_t launch_tile(const Prod &p, const Grid16 &gr, bool ad, bool bd, hipStream_t stream) {
     constexpr int NT = 64 * (BM / WM) * (BN / WN);
     const dim3 grid(gr.tiles_m * gr.tiles_n, gr.slices);
     if (ad && bd)
-        hipLaunchKernelGGL((prod16_kernel<DT, BM, BN, WM, WN, AMC, BMC, true, true>), grid,
+        hipLaunchKernelGGL((prod16_kernel<DT, BM, BN, WM, WN, NBUF, AMC, BMC, true, true>), grid,
                            dim3(NT), 0, stream, p, gr);
     else if (ad && BMC)   // the backward products: G is laid out for direct loads, B may not be
-        hipLaunchKernelGGL((prod16_kernel<DT, BM, BN, WM, WN, AMC, BMC, BMC != 0, false>), grid,
+        hipLaunchKernelGGL((prod16_kernel<DT, BM, BN, WM, WN, NBUF, AMC, BMC, BMC != 0, false>), grid,
                            dim3(NT), 0, stream, p, gr);
     else
-        hipLaunchKernelGGL((prod16_kernel<DT, BM, BN, WM, WN, AMC, BMC, false, false>), grid,
+        hipLaunchKernelGGL((prod16_kernel<DT, BM, BN, WM, WN, NBUF, AMC, BMC, false, false>), grid,
                            dim3(NT), 0, stream, p, gr);
     return hipGetLastError();
 }
 
-template <int DT, int BM, int BN, int WM, int WN>
+template <int DT, int BM, int BN, int WM, int WN, int NBUF>
 hipError_t launch_layout(const Prod &p, const Grid16 &gr, bool ad, bool bd, hipStream_t stream) {
-    if (!p.b_mc) return launch_tile<DT, BM, BN, WM, WN, 0, 0>(p, gr, ad, bd, stream);
-    if (!p.a_mc) return launch_tile<DT, BM, BN, WM, WN, 0, 1>(p, gr, ad, bd, stream);
-    return launch_tile<DT, BM, BN, WM, WN, 1, 1>(p, gr, ad, bd, stream);
+    if (!p.b_mc) return launch_tile<DT, BM, BN, WM, WN, NBUF, 0, 0>(p, gr, ad, bd, stream);
+    if (!p.a_mc) return launch_tile<DT, BM, BN, WM, WN, NBUF, 0, 1>(p, gr, ad, bd, stream);
+    return launch_tile<DT, BM, BN, WM, WN, NBUF, 1, 1>(p, gr, ad, bd, stream);
 }
 
 template <int DT>
@@ -358,8 +379,8 @@ hipError_t launch_dt(Prod p, const Workspace &ws, hipStream_t stream) {
     gr.count = ws.counters;
     const bool ad = direct_ok(p.A, p.lda, p.a_pad ? 0 : p.a_mc ? p.M : p.K, q.bm, p.a_mc);
     const bool bd = direct_ok(p.B, p.ldb, p.b_mc ? p.N : p.K, q.bn, p.b_mc);
-    if (q.bm == 128) return launch_layout<DT, 128, 128, 64, 64>(p, gr, ad, bd, stream);
-    return launch_layout<DT, 64, 64, 32, 32>(p, gr, ad, bd, stream);
+    if (q.bm == 128) return launch_layout<DT, 128, 128, 64, 64, 4>(p, gr, ad, bd, stream);
+    return launch_layout<DT, 64, 64, 32, 32, 4>(p, gr, ad, bd, stream);
 }
 
 }  // namespace

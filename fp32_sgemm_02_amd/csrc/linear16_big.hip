@@ -4,7 +4,8 @@
 //
 // Operands, images, row order and epilogue as in linear16.hip (k-contiguous
 // operands as swizzled rows, the others read transposed); what differs is the
-// schedule.  A wave owns 128 x 64 of C.  One stage (64 of k) of it is four
+// schedule.  A wave owns 128 x 64 of C (64 rows of
+// each half of the tile's, 32 columns of each half).  One stage (64 of k) of it is four
 // phases of 16 MFMAs, a quadrant each: with the halves A0, A1 of its rows and
 // B0, B1 of its columns,
 //     phase 0: A0 B0    1: A0 B1    2: A1 B1    3: A1 B0
@@ -35,28 +36,22 @@ constexpr int kHalf = kTile / 2 * kBK * 2;          // bytes of one half of an o
 constexpr int kStage = 4 * kHalf;                   // A0 A1 B0 B1
 constexpr int kOutOfRange = (int)0x80000000u;
 
-// One operand.  IS_A: halves of 64 rows of each of two 128-row wave tiles;
-// else of 32 rows of each of four 64-row wave tiles.  An image half holds
-// 128 tile rows in image order (k-contiguous) or, own index contiguous, 64
-// rows of k of 16 chunks of 8 tile rows.
+// One operand.  Its halves are rows 0 .. 127 and 128 .. 255 of the tile; of
+// each, a wave tile takes 64 rows (IS_A, two wave tiles) or 32 (four).  An
+// image half holds its rows in image order (k-contiguous) or, own index
+// contiguous, 64 rows of k of 16 chunks of 8 tile rows (256 bytes, which are
+// contiguous in memory too).
 template <int MC, bool IS_A>
 struct Half {
     int off[2][2], kk[2];
     const u16 *base;
     long long ld;
 
-    // tile row of row r of half h
+    // tile row of row r of half h: groups of four (two) blocks
     static __device__ __forceinline__ int tile_row(int h, int r) {
-        // 64-row groups of four blocks (image order): block b's row i is row
-        // 16 (i / 4) + 4 b + i % 4 of the group
-        const int in = r & (IS_A ? 63 : 31);
-        const int group = IS_A ? 2 * (r >> 6) + h : r >> 5;
-        const int b = (IS_A ? 0 : 2 * h) + (in >> 4), i = in & 15;
-        return 64 * group + 16 * (i >> 2) + 4 * b + (i & 3);
-    }
-    // first tile row of chunk c (8 rows) of half h
-    static __device__ __forceinline__ int tile_chunk(int h, int c) {
-        return IS_A ? 128 * (c >> 3) + 64 * h + 8 * (c & 7) : 16 * c + 8 * h;
+        constexpr int G = IS_A ? 4 : 2;
+        const int b = (r >> 4) & (G - 1), i = r & 15;
+        return 128 * h + (r & ~(16 * G - 1)) + 4 * G * (i >> 2) + 4 * b + (i & 3);
     }
     static __device__ __forceinline__ int swz(int k) {
         return IS_A ? ((k & 1) | ((k & 2) << 2)) : ((k & 3) << 2);
@@ -73,7 +68,7 @@ struct Half {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 if constexpr (MC) {
-                    const int k = q >> 4, row = tile_chunk(h, (q & 15) ^ swz(k));
+                    const int k = q >> 4, row = 128 * h + 8 * ((q & 15) ^ swz(k));
                     kk[j] = k;
                     off[h][j] = row >= lim ? kOutOfRange : (k * (int)ld + row) * 2;
                 } else {
@@ -237,18 +232,15 @@ __global__ void __launch_bounds__(512, 2) prod16_big_kernel(Prod p, GridBig gr) 
     wait(Zero{});   // no load of a stage past the end is left in flight
 
     const int i = lane & 15, g = lane >> 4;
-    with_act(p.act, [&](auto tag) {
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-            const int m = m0 + wm * 128 + 64 * (x >> 2) + 16 * (i >> 2) + 4 * (x & 3) + (i & 3);
-            if (m >= p.M) continue;
-            float v[16];
-#pragma unroll
-            for (int y = 0; y < 4; ++y)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) v[4 * y + r] = acc[y][x][r];
-            finish_run<DT, decltype(tag)::value>(p, m, n0 + wn * 64 + 16 * g, v);
-        }
+    with_act(p.act, [&](auto tag) __attribute__((always_inline)) {
+        each<16>([&](auto q) __attribute__((always_inline)) {
+            constexpr int x = q / 2, h = q % 2;
+            const int m = m0 + 128 * (x >> 2) + 64 * wm + 16 * (i >> 2) + 4 * (x & 3) + (i & 3);
+            const floatx4 u = acc[2 * h][x], w = acc[2 * h + 1][x];
+            const float v[8] = {u[0], u[1], u[2], u[3], w[0], w[1], w[2], w[3]};
+            if (m < p.M)
+                finish_run<DT, decltype(tag)::value>(p, m, n0 + 128 * h + 32 * wn + 8 * g, v);
+        });
     });
 #endif
 }
