@@ -202,12 +202,17 @@ __device__ __forceinline__ bool join_slices(const Grid16 &gr, int tile, int tile
 // LDS, one barrier per stage.  With direct loads NBUF - 1 stages are in flight
 // (those past the end read zeros, which touch no memory and keep the count of
 // outstanding loads); operands that pass through registers have two.
-template <int DT, int BM, int BN, int WM, int WN, int NBUF_, int AMC, int BMC, bool ADIR, bool BDIR>
+// KG: k-groups.  With two, two sets of waves own the same tile and each takes
+// one 32-k step of every stage, so that a SIMD has a second wave whose LDS
+// reads and loads run under the first one's products; at the end each set
+// hands half of its sums to the other through LDS and finishes the other half.
+template <int DT, int BM, int BN, int WM, int WN, int NBUF_, int KG, int AMC, int BMC,
+          bool ADIR, bool BDIR>
 __global__ void __launch_bounds__(512)   // at most 256 registers a lane: with more the compiler
                                          // keeps moving the accumulators between register files
 prod16_kernel(Prod p, Grid16 gr) {
 #ifdef __HIP_DEVICE_COMPILE__   // the host pass needs the launch stub only
-    constexpr int WAVES_N = BN / WN, NW = (BM / WM) * WAVES_N, NT = 64 * NW;
+    constexpr int WAVES_N = BN / WN, WAVES = (BM / WM) * WAVES_N, NW = WAVES * KG, NT = 64 * NW;
     constexpr int MB = WM / 16, NB = WN / 16;
     constexpr int GM = MB < 4 ? MB : 4, GN = NB < 4 ? NB : 4;
     using OpA = Operand<BM, AMC, ADIR, GM, NW>;
@@ -218,7 +223,7 @@ prod16_kernel(Prod p, Grid16 gr) {
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave / WAVES_N, wn = wave % WAVES_N;
+    const int kg = wave / WAVES, wm = wave % WAVES / WAVES_N, wn = wave % WAVES_N;
     const int tiles = gr.tiles_m * gr.tiles_n;
     const int slice = blockIdx.y;
     int tm, tn;
@@ -265,7 +270,8 @@ prod16_kernel(Prod p, Grid16 gr) {
         pipeline_fence();
         issue(t + AHEAD, nxt);
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
+        for (int q = 0; q < 2 / KG; ++q) {
+            const int s = KG == 2 ? kg : q;
             uintx4 fa[MB], fb[NB];
 #pragma unroll
             for (int x = 0; x < MB; ++x) fa[x] = OpA::frag(cur, wm * MB + x, s, lane);
@@ -279,26 +285,60 @@ prod16_kernel(Prod p, Grid16 gr) {
         slot = slot + 1 == NBUF ? 0 : slot + 1;
     }
     wait_loads<0>();   // no load of a stage past the end is left in flight
+    // Row blocks [x0, x0 + XB) are this wave's to finish.
+    constexpr int XB = MB / KG;
+    const int x0 = KG == 2 ? kg * XB : 0;
+    floatx4 sum[NB][XB];
+    if constexpr (KG == 2) {
+        static_assert(NT / 2 * NB * XB * 16 <= (int)sizeof(smem) / 2, "both halves fit the ring");
+        __syncthreads();
+        // the other set's blocks, as [set][block][thread of the set]
+        floatx4 *box = reinterpret_cast<floatx4 *>(smem);
+        const int th = tid % (NT / 2);
+        each<NB * XB>([&](auto j) __attribute__((always_inline)) {
+            const floatx4 lo = acc[j / XB][j % XB], hi = acc[j / XB][XB + j % XB];
+            box[(kg * NB * XB + j) * (NT / 2) + th] = kg ? lo : hi;
+            sum[j / XB][j % XB] = kg ? hi : lo;
+        });
+        __syncthreads();
+        each<NB * XB>([&](auto j) __attribute__((always_inline)) {
+            const floatx4 v = box[((1 - kg) * NB * XB + j) * (NT / 2) + th];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[j / XB][j % XB][e] += v[e];
+        });
+    } else {
+#pragma unroll
+        for (int y = 0; y < NB; ++y)
+#pragma unroll
+            for (int x = 0; x < XB; ++x) sum[y][x] = acc[y][x];
+    }
     // (the flag of the join is in the free ring: with a second LDS object the
     // compiler has the fragment reads wait for every direct load)
     if (gr.slices > 1 &&
-        !join_slices<NB, MB, NT>(gr, tile, tiles, slice, tid, reinterpret_cast<int *>(smem[0]), acc))
+        !join_slices<NB, XB, NT>(gr, tile, tiles, slice, tid, reinterpret_cast<int *>(smem[0]), sum))
         return;
 
+    // The epilogue as a loop, each lane's sums passing through its own place in
+    // the free ring (unrolled it takes the same time and several times the code).
+    __syncthreads();
     const int i = lane & 15, g = lane >> 4;
+    floatx4 *own = reinterpret_cast<floatx4 *>(smem) + tid;
+    each<XB * NB>([&](auto j) __attribute__((always_inline)) { own[j * NT] = sum[j % NB][j / NB]; });
     with_act(p.act, [&](auto tag) __attribute__((always_inline)) {
-        constexpr int ACT = decltype(tag)::value;
-        each<MB * (NB / GN)>([&](auto c) __attribute__((always_inline)) {
-            constexpr int x = c / (NB / GN), q = c % (NB / GN);
+#pragma unroll 1
+        for (int c = 0; c < XB * (NB / GN); ++c) {
+            const int x = x0 + c / (NB / GN), q = c % (NB / GN);
             const int m = m0 + wm * WM + 16 * GM * (x / GM) + 4 * GM * (i >> 2) + 4 * (x % GM) + (i & 3);
             float v[4 * GN];
 #pragma unroll
-            for (int y = 0; y < GN; ++y)
+            for (int y = 0; y < GN; ++y) {
+                const floatx4 u = own[(c * GN + y) * NT];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) v[4 * y + r] = acc[q * GN + y][x][r];
+                for (int r = 0; r < 4; ++r) v[4 * y + r] = u[r];
+            }
             if (m < p.M)
-                finish_run<DT, ACT>(p, m, n0 + wn * WN + 16 * GN * q + 4 * GN * g, v);
-        });
+                finish_run<DT, decltype(tag)::value>(p, m, n0 + wn * WN + 16 * GN * q + 4 * GN * g, v);
+        }
     });
 #endif
 }
@@ -328,8 +368,8 @@ Plan16 plan16(const Prod &p) {
     const long long t = tiles(q.bm);
     const int stages = p.fold ? 2 : (p.K + kBK - 1) / kBK;
     int s = 1;
-    if (!p.fold && !q.big && t < 2 * kCUs && t <= kWorkspaceCounters) {
-        s = (int)((2 * kCUs + t - 1) / t);
+    if (!p.fold && !q.big && t <= kCUs / 2) {
+        s = (int)(kCUs / t);
         const int most = stages / 4;
         if (s > most) s = most;
         if (s > 32) s = 32;
@@ -341,27 +381,27 @@ Plan16 plan16(const Prod &p) {
     return q;
 }
 
-template <int DT, int BM, int BN, int WM, int WN, int NBUF, int AMC, int BMC>
+template <int DT, int BM, int BN, int WM, int WN, int NBUF, int KG, int AMC, int BMC>
 hipError_t launch_tile(const Prod &p, const Grid16 &gr, bool ad, bool bd, hipStream_t stream) {
-    constexpr int NT = 64 * (BM / WM) * (BN / WN);
+    constexpr int NT = 64 * (BM / WM) * (BN / WN) * KG;
     const dim3 grid(gr.tiles_m * gr.tiles_n, gr.slices);
     if (ad && bd)
-        hipLaunchKernelGGL((prod16_kernel<DT, BM, BN, WM, WN, NBUF, AMC, BMC, true, true>), grid,
+        hipLaunchKernelGGL((prod16_kernel<DT, BM, BN, WM, WN, NBUF, KG, AMC, BMC, true, true>), grid,
                            dim3(NT), 0, stream, p, gr);
     else if (ad && BMC)   // the backward products: G is laid out for direct loads, B may not be
-        hipLaunchKernelGGL((prod16_kernel<DT, BM, BN, WM, WN, NBUF, AMC, BMC, BMC != 0, false>), grid,
+        hipLaunchKernelGGL((prod16_kernel<DT, BM, BN, WM, WN, NBUF, KG, AMC, BMC, BMC != 0, false>), grid,
                            dim3(NT), 0, stream, p, gr);
     else
-        hipLaunchKernelGGL((prod16_kernel<DT, BM, BN, WM, WN, NBUF, AMC, BMC, false, false>), grid,
+        hipLaunchKernelGGL((prod16_kernel<DT, BM, BN, WM, WN, NBUF, KG, AMC, BMC, false, false>), grid,
                            dim3(NT), 0, stream, p, gr);
     return hipGetLastError();
 }
 
-template <int DT, int BM, int BN, int WM, int WN, int NBUF>
+template <int DT, int BM, int BN, int WM, int WN, int NBUF, int KG>
 hipError_t launch_layout(const Prod &p, const Grid16 &gr, bool ad, bool bd, hipStream_t stream) {
-    if (!p.b_mc) return launch_tile<DT, BM, BN, WM, WN, NBUF, 0, 0>(p, gr, ad, bd, stream);
-    if (!p.a_mc) return launch_tile<DT, BM, BN, WM, WN, NBUF, 0, 1>(p, gr, ad, bd, stream);
-    return launch_tile<DT, BM, BN, WM, WN, NBUF, 1, 1>(p, gr, ad, bd, stream);
+    if (!p.b_mc) return launch_tile<DT, BM, BN, WM, WN, NBUF, KG, 0, 0>(p, gr, ad, bd, stream);
+    if (!p.a_mc) return launch_tile<DT, BM, BN, WM, WN, NBUF, KG, 0, 1>(p, gr, ad, bd, stream);
+    return launch_tile<DT, BM, BN, WM, WN, NBUF, KG, 1, 1>(p, gr, ad, bd, stream);
 }
 
 template <int DT>
@@ -379,8 +419,8 @@ hipError_t launch_dt(Prod p, const Workspace &ws, hipStream_t stream) {
     gr.count = ws.counters;
     const bool ad = direct_ok(p.A, p.lda, p.a_pad ? 0 : p.a_mc ? p.M : p.K, q.bm, p.a_mc);
     const bool bd = direct_ok(p.B, p.ldb, p.b_mc ? p.N : p.K, q.bn, p.b_mc);
-    if (q.bm == 128) return launch_layout<DT, 128, 128, 64, 64, 4>(p, gr, ad, bd, stream);
-    return launch_layout<DT, 64, 64, 32, 32, 4>(p, gr, ad, bd, stream);
+    if (q.bm == 128) return launch_layout<DT, 128, 128, 64, 64, 4, 2>(p, gr, ad, bd, stream);
+    return launch_layout<DT, 64, 64, 32, 32, 4, 2>(p, gr, ad, bd, stream);
 }
 
 }  // namespace

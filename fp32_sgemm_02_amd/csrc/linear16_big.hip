@@ -231,15 +231,26 @@ __global__ void __launch_bounds__(512, 2) prod16_big_kernel(Prod p, GridBig gr) 
     if (wave < 4) barrier();
     wait(Zero{});   // no load of a stage past the end is left in flight
 
+    // The epilogue runs as a loop over the row blocks, a column half at a time,
+    // each lane's sums passing through its own place in the free ring.
+    // Unrolled, as registers would need, it takes the same time and several
+    // times the code.
+    barrier();   // no wave reads the ring any more
     const int i = lane & 15, g = lane >> 4;
-    with_act(p.act, [&](auto tag) __attribute__((always_inline)) {
-        each<16>([&](auto q) __attribute__((always_inline)) {
-            constexpr int x = q / 2, h = q % 2;
-            const int m = m0 + 128 * (x >> 2) + 64 * wm + 16 * (i >> 2) + 4 * (x & 3) + (i & 3);
-            const floatx4 u = acc[2 * h][x], w = acc[2 * h + 1][x];
-            const float v[8] = {u[0], u[1], u[2], u[3], w[0], w[1], w[2], w[3]};
-            if (m < p.M)
-                finish_run<DT, decltype(tag)::value>(p, m, n0 + 128 * h + 32 * wn + 8 * g, v);
+    floatx4 *box = reinterpret_cast<floatx4 *>(smem) + wave * 16 * 64 + lane;
+    each<2>([&](auto h) __attribute__((always_inline)) {
+        each<16>([&](auto j) __attribute__((always_inline)) {
+            box[j * 64] = acc[2 * h + j % 2][j / 2];
+        });
+        const int n = n0 + 128 * h + 32 * wn + 8 * g;
+        with_act(p.act, [&](auto tag) __attribute__((always_inline)) {
+#pragma unroll 1
+            for (int x = 0; x < 8; ++x) {
+                const int m = m0 + 128 * (x >> 2) + 64 * wm + 16 * (i >> 2) + 4 * (x & 3) + (i & 3);
+                const floatx4 u = box[x * 128], w = box[x * 128 + 64];
+                const float v[8] = {u[0], u[1], u[2], u[3], w[0], w[1], w[2], w[3]};
+                if (m < p.M) finish_run<DT, decltype(tag)::value>(p, m, n, v);
+            }
         });
     });
 #endif
