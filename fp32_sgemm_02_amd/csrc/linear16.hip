@@ -17,20 +17,13 @@
 // lane j fetches four values of row j / 4 and receives, as its four results,
 // value i = j of those four rows, so two reads give the 8 k values of a
 // fragment.  The chunks of those rows are swizzled by k (mc_swz) so that the
-// 16 lanes of a group touch 16 different bank pairs.
-//
-// Row order.  MFMA row and column indices are free labels, so index i of block
-// b within a group of G blocks stands for row 4G (i / 4) + 4b + i % 4 of the
-// group: a lane then holds 4G adjacent columns of one row of C over the G
-// blocks, and stores them 16 bytes at a time.
+// 32 lanes served at a time touch all banks once.
 #include "linear_internal.hpp"
 
 namespace sg {
 namespace {
 
 typedef __attribute__((address_space(3))) void lds_void;
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef s16x4 __attribute__((address_space(3))) lds_s16x4;
 
 constexpr int kBK = 64;                            // k per stage
 constexpr int kOutOfRange = (int)0x80000000u;      // a buffer offset that reads zero
@@ -42,34 +35,28 @@ __device__ __forceinline__ void wait_loads() {
     __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
 }
 
-// Tile row held in image row r, groups of G 16-row blocks.
-template <int G>
-__device__ __forceinline__ int image_row(int r) {
-    return (r & ~(16 * G - 1)) | (4 * G * ((r & 15) >> 2) + 4 * ((r >> 4) & (G - 1)) + (r & 3));
-}
-
 // Swizzle of the 16-byte chunks of row k of an own-index-contiguous image of
-// BT columns read in groups of G blocks: the four rows of one transposing read
-// (k mod 4) are moved to chunks that the others' reads do not touch.
-template <int BT, int G>
+// BT columns.  32 lanes of a transposing read (two groups of 16) fetch 32
+// bytes of each of the rows k, k+1, k+2, k+3 and k+8 .. k+11: the swizzle moves
+// these to eight different 32-byte places of the 256 bytes of the banks.
+// (Moving only the four rows of one group apart cost as many cycles again:
+// SQ_LDS_BANK_CONFLICT 2 per read, 0 with this one.)
+template <int BT>
 __device__ __forceinline__ int mc_swz(int k) {
-    constexpr int C = BT / 8;   // chunks per row
-    if constexpr (C >= 16)
-        return G == 4 ? ((k & 1) | ((k & 2) << 2)) : G == 2 ? ((k & 3) << 2) : ((k & 3) << 1);
-    else if constexpr (C == 8)   // rows of 128 bytes: neighbours are 128 bytes apart already
-        return G == 4 ? ((k >> 1) & 1) : G == 2 ? (((k >> 1) & 1) << 2) : (((k >> 1) & 1) << 1);
-    else
-        return 0;
+    if constexpr (BT >= 128)
+        return 2 * ((k & 3) | ((k >> 1) & 4));
+    else   // rows of 128 bytes: every other row is 128 bytes apart already
+        return 2 * (((k >> 1) & 1) | ((k >> 2) & 2));
 }
 
 // One operand's tile: BT rows, stored k-contiguous (MC = 0) or with its own
-// index contiguous (MC = 1), read in groups of G blocks by NW waves' loads.
+// index contiguous (MC = 1), loaded by NW waves.
 // DIRECT: 16-byte rows throughout, copied to LDS by direct loads (a chunk
 // outside the matrix reads as zero: its buffer offset is out of range).
 // Otherwise the chunks pass through registers, from any 2-byte alignment
 // (the target loads 16 bytes from any address), those that straddle an edge
 // value by value.
-template <int BT, int MC, bool DIRECT, int G, int NW>
+template <int BT, int MC, bool DIRECT, int NW>
 struct Operand {
     static constexpr int BYTES = BT * kBK * 2;
     static constexpr int L = BT * 8 / (64 * NW);   // 16-byte chunks per lane and stage
@@ -92,12 +79,12 @@ struct Operand {
         for (int j = 0; j < L; ++j) {
             const int q = (j * NW + wave) * 64 + lane;   // chunk of the image
             if constexpr (MC) {
-                const int k = q / (BT / 8), c = (q % (BT / 8)) ^ mc_swz<BT, G>(k);
+                const int k = q / (BT / 8), c = (q % (BT / 8)) ^ mc_swz<BT>(k);
                 kk[j] = k;
                 cc[j] = 8 * c;
                 off[j] = 8 * c >= lim ? kOutOfRange : (k * (int)ld + 8 * c) * 2;
             } else {
-                const int r = q / 8, c = (q % 8) ^ ((r >> 1) & 7), row = image_row<G>(r);
+                const int r = q / 8, c = (q % 8) ^ ((r >> 1) & 7), row = r;
                 kk[j] = 8 * c;
                 cc[j] = row;
                 off[j] = row >= lim ? kOutOfRange : (row * (int)ld + 8 * c) * 2;
@@ -144,24 +131,31 @@ struct Operand {
         }
     }
 
-    // Fragment of 16-row block `blk` (counted from the tile's first row) and
-    // 32-k step s.
-    static __device__ __forceinline__ uintx4 frag(const unsigned char *img, int blk, int s,
-                                                  int lane) {
+    // Fragments of the BLOCKS 16-row blocks from `blk` on (counted from the
+    // tile's first row), 32-k step s.
+    template <int BLOCKS>
+    static __device__ __forceinline__ void read(const unsigned char *img, int blk, int s, int lane,
+                                                uintx4 (&f)[BLOCKS]) {
         const int i = lane & 15, g = lane >> 4;
         if constexpr (MC) {
-            const int col = 16 * G * (blk / G) + 4 * G * (i & 3) + 4 * (blk % G);
             const int k = 32 * s + 8 * g + (i >> 2);   // and k + 4: the same swizzle
-            const int at = k * (BT * 2) + (((col >> 3) ^ mc_swz<BT, G>(k)) << 4) + ((col & 4) << 1);
-            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(img + at));
-            const s16x4 hi =
-                __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(img + at + 4 * BT * 2));
-            const uintx2 l = __builtin_bit_cast(uintx2, lo), h = __builtin_bit_cast(uintx2, hi);
-            return uintx4{l[0], l[1], h[0], h[1]};
+            unsigned at[BLOCKS];
+            uintx4 r[BLOCKS][1];
+#pragma unroll
+            for (int b = 0; b < BLOCKS; ++b) {
+                const int chunk = 2 * (blk + b) + ((i >> 1) & 1);
+                at[b] = lds_address(img) + k * (BT * 2) + ((chunk ^ mc_swz<BT>(k)) << 4) + ((i & 1) << 3);
+            }
+            read_transposed<BLOCKS, 1, 4 * BT * 2, 0>(at, r);
+#pragma unroll
+            for (int b = 0; b < BLOCKS; ++b) f[b] = r[b][0];
         } else {
-            const int r = 16 * blk + i;
-            return *reinterpret_cast<const uintx4 *>(img + r * 128 +
-                                                     (((4 * s + g) ^ ((r >> 1) & 7)) << 4));
+#pragma unroll
+            for (int b = 0; b < BLOCKS; ++b) {
+                const int r = 16 * (blk + b) + i;
+                f[b] = *reinterpret_cast<const uintx4 *>(img + r * 128 +
+                                                         (((4 * s + g) ^ ((r >> 1) & 7)) << 4));
+            }
         }
     }
 };
@@ -214,9 +208,8 @@ prod16_kernel(Prod p, Grid16 gr) {
 #ifdef __HIP_DEVICE_COMPILE__   // the host pass needs the launch stub only
     constexpr int WAVES_N = BN / WN, WAVES = (BM / WM) * WAVES_N, NW = WAVES * KG, NT = 64 * NW;
     constexpr int MB = WM / 16, NB = WN / 16;
-    constexpr int GM = MB < 4 ? MB : 4, GN = NB < 4 ? NB : 4;
-    using OpA = Operand<BM, AMC, ADIR, GM, NW>;
-    using OpB = Operand<BN, BMC, BDIR, GN, NW>;
+    using OpA = Operand<BM, AMC, ADIR, NW>;
+    using OpB = Operand<BN, BMC, BDIR, NW>;
     constexpr int NBUF = ADIR && BDIR ? NBUF_ : 2;
     constexpr int AHEAD = NBUF - 1;   // stages in flight
     __shared__ __attribute__((aligned(1024))) unsigned char smem[NBUF][OpA::BYTES + OpB::BYTES];
@@ -273,10 +266,8 @@ prod16_kernel(Prod p, Grid16 gr) {
         for (int q = 0; q < 2 / KG; ++q) {
             const int s = KG == 2 ? kg : q;
             uintx4 fa[MB], fb[NB];
-#pragma unroll
-            for (int x = 0; x < MB; ++x) fa[x] = OpA::frag(cur, wm * MB + x, s, lane);
-#pragma unroll
-            for (int y = 0; y < NB; ++y) fb[y] = OpB::frag(cur + OpA::BYTES, wn * NB + y, s, lane);
+            OpA::template read<MB>(cur, wm * MB, s, lane, fa);
+            OpB::template read<NB>(cur + OpA::BYTES, wn * NB, s, lane, fb);
 #pragma unroll
             for (int y = 0; y < NB; ++y)
 #pragma unroll
@@ -318,28 +309,10 @@ prod16_kernel(Prod p, Grid16 gr) {
         !join_slices<NB, XB, NT>(gr, tile, tiles, slice, tid, reinterpret_cast<int *>(smem[0]), sum))
         return;
 
-    // The epilogue as a loop, each lane's sums passing through its own place in
-    // the free ring (unrolled it takes the same time and several times the code).
-    __syncthreads();
-    const int i = lane & 15, g = lane >> 4;
-    floatx4 *own = reinterpret_cast<floatx4 *>(smem) + tid;
-    each<XB * NB>([&](auto j) __attribute__((always_inline)) { own[j * NT] = sum[j % NB][j / NB]; });
-    with_act(p.act, [&](auto tag) __attribute__((always_inline)) {
-#pragma unroll 1
-        for (int c = 0; c < XB * (NB / GN); ++c) {
-            const int x = x0 + c / (NB / GN), q = c % (NB / GN);
-            const int m = m0 + wm * WM + 16 * GM * (x / GM) + 4 * GM * (i >> 2) + 4 * (x % GM) + (i & 3);
-            float v[4 * GN];
-#pragma unroll
-            for (int y = 0; y < GN; ++y) {
-                const floatx4 u = own[(c * GN + y) * NT];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) v[4 * y + r] = u[r];
-            }
-            if (m < p.M)
-                finish_run<DT, decltype(tag)::value>(p, m, n0 + wn * WN + 16 * GN * q + 4 * GN * g, v);
-        }
-    });
+    __syncthreads();   // the ring is free
+    finish_wave<DT, XB, NB>(p, m0 + wm * WM + 16 * x0, n0 + wn * WN, lane,
+                            reinterpret_cast<float *>(smem) + wave * XB * NB * 256,
+                            [&](auto y, auto x) __attribute__((always_inline)) { return sum[y][x]; });
 #endif
 }
 

@@ -28,8 +28,6 @@ namespace sg {
 namespace {
 
 typedef __attribute__((address_space(3))) void lds_void;
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef s16x4 __attribute__((address_space(3))) lds_s16x4;
 
 constexpr int kBK = 64, kTile = 256;
 constexpr int kHalf = kTile / 2 * kBK * 2;          // bytes of one half of an operand's stage
@@ -38,7 +36,7 @@ constexpr int kOutOfRange = (int)0x80000000u;
 
 // One operand.  Its halves are rows 0 .. 127 and 128 .. 255 of the tile; of
 // each, a wave tile takes 64 rows (IS_A, two wave tiles) or 32 (four).  An
-// image half holds its rows in image order (k-contiguous) or, own index
+// image half holds its rows (k-contiguous) or, own index
 // contiguous, 64 rows of k of 16 chunks of 8 tile rows (256 bytes, which are
 // contiguous in memory too).
 template <int MC, bool IS_A>
@@ -47,15 +45,8 @@ struct Half {
     const u16 *base;
     long long ld;
 
-    // tile row of row r of half h: groups of four (two) blocks
-    static __device__ __forceinline__ int tile_row(int h, int r) {
-        constexpr int G = IS_A ? 4 : 2;
-        const int b = (r >> 4) & (G - 1), i = r & 15;
-        return 128 * h + (r & ~(16 * G - 1)) + 4 * G * (i >> 2) + 4 * b + (i & 3);
-    }
-    static __device__ __forceinline__ int swz(int k) {
-        return IS_A ? ((k & 1) | ((k & 2) << 2)) : ((k & 3) << 2);
-    }
+    // see mc_swz in linear16.hip
+    static __device__ __forceinline__ int swz(int k) { return 2 * ((k & 3) | ((k >> 1) & 4)); }
 
     __device__ __forceinline__ void init(const u16 *P, long long ld_, int row0, int rows, int wave,
                                          int lane) {
@@ -72,7 +63,7 @@ struct Half {
                     kk[j] = k;
                     off[h][j] = row >= lim ? kOutOfRange : (k * (int)ld + row) * 2;
                 } else {
-                    const int r = q >> 3, c = (q & 7) ^ ((r >> 1) & 7), row = tile_row(h, r);
+                    const int r = q >> 3, c = (q & 7) ^ ((r >> 1) & 7), row = 128 * h + r;
                     kk[j] = 8 * c;
                     off[h][j] = row >= lim ? kOutOfRange : (row * (int)ld + 8 * c) * 2;
                 }
@@ -89,22 +80,29 @@ struct Half {
                 r, (lds_void *)(img + (j * 8 + wave) * 1024), 16,
                 kk[j] >= krem ? kOutOfRange : off[h][j], 0, 0, 0);
     }
-    // Fragment of block b of wave tile w's part of a half, 32-k step s.
-    static __device__ __forceinline__ uintx4 frag(const unsigned char *img, int w, int b, int s,
-                                                  int lane) {
+    // Fragments of wave tile w's BLOCKS blocks of a half, both 32-k steps.
+    template <int BLOCKS>
+    static __device__ __forceinline__ void read(const unsigned char *img, int w, int lane,
+                                                uintx4 (&f)[BLOCKS][2]) {
         const int i = lane & 15, g = lane >> 4;
         if constexpr (MC) {
-            const int chunk = IS_A ? 8 * w + 2 * (i & 3) + (b >> 1) : 4 * w + (i & 3);
-            const int k = 32 * s + 8 * g + (i >> 2);
-            const int at = k * 256 + ((chunk ^ swz(k)) << 4) + ((b & 1) << 3);
-            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(img + at));
-            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(img + at + 1024));
-            const uintx2 l = __builtin_bit_cast(uintx2, lo), u = __builtin_bit_cast(uintx2, hi);
-            return uintx4{l[0], l[1], u[0], u[1]};
+            const int k = 8 * g + (i >> 2);   // and k + 4, k + 32, k + 36: the same swizzle
+            unsigned at[BLOCKS];
+#pragma unroll
+            for (int b = 0; b < BLOCKS; ++b) {
+                const int chunk = 2 * (BLOCKS * w + b) + ((i >> 1) & 1);
+                at[b] = lds_address(img) + k * 256 + ((chunk ^ swz(k)) << 4) + ((i & 1) << 3);
+            }
+            read_transposed<BLOCKS, 2, 1024, 8192>(at, f);
         } else {
-            const int r = (IS_A ? 64 : 32) * w + 16 * b + i;
-            return *reinterpret_cast<const uintx4 *>(img + r * 128 +
-                                                     (((4 * s + g) ^ ((r >> 1) & 7)) << 4));
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int b = 0; b < BLOCKS; ++b) {
+                    const int r = 16 * (BLOCKS * w + b) + i;
+                    f[b][s] = *reinterpret_cast<const uintx4 *>(
+                        img + r * 128 + (((4 * s + g) ^ ((r >> 1) & 7)) << 4));
+                }
         }
     }
 };
@@ -164,19 +162,9 @@ __global__ void __launch_bounds__(512, 2) prod16_big_kernel(Prod p, GridBig gr) 
     auto load_b = [&](int h, int t) { b.issue(h, t, p.K - t * kBK, image(t, 2 + h), wave); };
 
     uintx4 fa[4][2], f0[2][2], f1[2][2], g0[2][2];
-    auto read_a = [&](int h, int t) {
-        const unsigned char *img = image(t, h);
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) fa[x][s] = OpA::frag(img, wm, x, s, lane);
-    };
+    auto read_a = [&](int h, int t) { OpA::template read<4>(image(t, h), wm, lane, fa); };
     auto read_b = [&](int h, int t, uintx4 (&f)[2][2]) {
-        const unsigned char *img = image(t, 2 + h);
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int y = 0; y < 2; ++y) f[y][s] = OpB::frag(img, wn, y, s, lane);
+        OpB::template read<2>(image(t, 2 + h), wn, lane, f);
     };
     auto compute = [&](int ha, int hb, const uintx4 (&f)[2][2]) {
         barrier();
@@ -194,20 +182,20 @@ __global__ void __launch_bounds__(512, 2) prod16_big_kernel(Prod p, GridBig gr) 
     };
     // stage t with B0 in f; leaves B0 of stage t + 1 in g
     auto stage = [&](int t, const uintx4 (&f)[2][2], uintx4 (&g)[2][2]) {
-        read_a(0, t);
         load_b(0, t + 2);
+        read_a(0, t);
         wait(Twelve{});
         compute(0, 0, f);
-        read_b(1, t, f1);
         load_a(0, t + 2);
+        read_b(1, t, f1);
         wait(Twelve{});
         compute(0, 1, f1);
-        read_a(1, t);
         load_b(1, t + 2);
+        read_a(1, t);
         wait(Twelve{});
         compute(1, 1, f1);
-        read_b(0, t + 1, g);
         load_a(1, t + 2);
+        read_b(0, t + 1, g);
         wait(Twelve{});
         compute(1, 0, f);
     };
@@ -231,27 +219,14 @@ __global__ void __launch_bounds__(512, 2) prod16_big_kernel(Prod p, GridBig gr) 
     if (wave < 4) barrier();
     wait(Zero{});   // no load of a stage past the end is left in flight
 
-    // The epilogue runs as a loop over the row blocks, a column half at a time,
-    // each lane's sums passing through its own place in the free ring.
-    // Unrolled, as registers would need, it takes the same time and several
-    // times the code.
     barrier();   // no wave reads the ring any more
-    const int i = lane & 15, g = lane >> 4;
-    floatx4 *box = reinterpret_cast<floatx4 *>(smem) + wave * 16 * 64 + lane;
-    each<2>([&](auto h) __attribute__((always_inline)) {
-        each<16>([&](auto j) __attribute__((always_inline)) {
-            box[j * 64] = acc[2 * h + j % 2][j / 2];
-        });
-        const int n = n0 + 128 * h + 32 * wn + 8 * g;
-        with_act(p.act, [&](auto tag) __attribute__((always_inline)) {
-#pragma unroll 1
-            for (int x = 0; x < 8; ++x) {
-                const int m = m0 + 128 * (x >> 2) + 64 * wm + 16 * (i >> 2) + 4 * (x & 3) + (i & 3);
-                const floatx4 u = box[x * 128], w = box[x * 128 + 64];
-                const float v[8] = {u[0], u[1], u[2], u[3], w[0], w[1], w[2], w[3]};
-                if (m < p.M) finish_run<DT, decltype(tag)::value>(p, m, n, v);
-            }
-        });
+    float *box = reinterpret_cast<float *>(smem) + wave * (kStage / 16);   // 16 KB a wave
+    each<4>([&](auto c) __attribute__((always_inline)) {
+        constexpr int h = c / 2, v = c % 2;   // column half, row half
+        finish_wave<DT, 4, 2>(p, m0 + 128 * v + 64 * wm, n0 + 128 * h + 32 * wn, lane, box + v * 2048,
+                              [&](auto y, auto x) __attribute__((always_inline)) {
+                                  return acc[2 * h + y][4 * v + x];
+                              });
     });
 #endif
 }

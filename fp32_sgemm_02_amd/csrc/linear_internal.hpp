@@ -190,6 +190,91 @@ __device__ __forceinline__ floatx4 mfma16(uintx4 a, uintx4 b, floatx4 c) {
                                                       __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
 }
 
+// Transposing LDS reads of 16-bit values, with their wait in the same asm block
+// (the builtin would have each read wait for every direct load in flight, since
+// the compiler cannot tell the stages of the ring apart: 4096^3 with one operand
+// read this way: 8192^3 dX 892 us, 752 with this).  at[b]: LDS address of block b's part for this
+// lane; HI: bytes from its first four rows of k to the next four; with STEPS ==
+// 2 also the next 32-k step, NEXT bytes further.  f[b][s]: the fragments.
+template <int BLOCKS, int STEPS, int HI, int NEXT>
+__device__ __forceinline__ void read_transposed(const unsigned (&at)[BLOCKS],
+                                                uintx4 (&f)[BLOCKS][STEPS]) {
+    static_assert((BLOCKS == 2 || BLOCKS == 4) && (STEPS == 1 || STEPS == 2), "2 or 4 blocks");
+    uintx2 r[BLOCKS][STEPS][2];
+    if constexpr (BLOCKS == 2 && STEPS == 1) {
+        asm volatile(
+            "ds_read_b64_tr_b16 %0, %4\n"
+            "ds_read_b64_tr_b16 %1, %4 offset:%6\n"
+            "ds_read_b64_tr_b16 %2, %5\n"
+            "ds_read_b64_tr_b16 %3, %5 offset:%6\n"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(r[0][0][0]), "=&v"(r[0][0][1]), "=&v"(r[1][0][0]), "=&v"(r[1][0][1])
+            : "v"(at[0]), "v"(at[1]), "n"(HI)
+            : "memory");
+    } else if constexpr (BLOCKS == 2 && STEPS == 2) {
+        asm volatile(
+            "ds_read_b64_tr_b16 %0, %8\n"
+            "ds_read_b64_tr_b16 %1, %8 offset:%10\n"
+            "ds_read_b64_tr_b16 %2, %8 offset:%11\n"
+            "ds_read_b64_tr_b16 %3, %8 offset:%12\n"
+            "ds_read_b64_tr_b16 %4, %9\n"
+            "ds_read_b64_tr_b16 %5, %9 offset:%10\n"
+            "ds_read_b64_tr_b16 %6, %9 offset:%11\n"
+            "ds_read_b64_tr_b16 %7, %9 offset:%12\n"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(r[0][0][0]), "=&v"(r[0][0][1]), "=&v"(r[0][1][0]), "=&v"(r[0][1][1]), "=&v"(r[1][0][0]), "=&v"(r[1][0][1]), "=&v"(r[1][1][0]), "=&v"(r[1][1][1])
+            : "v"(at[0]), "v"(at[1]), "n"(HI), "n"(NEXT), "n"(NEXT + HI)
+            : "memory");
+    } else if constexpr (BLOCKS == 4 && STEPS == 1) {
+        asm volatile(
+            "ds_read_b64_tr_b16 %0, %8\n"
+            "ds_read_b64_tr_b16 %1, %8 offset:%12\n"
+            "ds_read_b64_tr_b16 %2, %9\n"
+            "ds_read_b64_tr_b16 %3, %9 offset:%12\n"
+            "ds_read_b64_tr_b16 %4, %10\n"
+            "ds_read_b64_tr_b16 %5, %10 offset:%12\n"
+            "ds_read_b64_tr_b16 %6, %11\n"
+            "ds_read_b64_tr_b16 %7, %11 offset:%12\n"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(r[0][0][0]), "=&v"(r[0][0][1]), "=&v"(r[1][0][0]), "=&v"(r[1][0][1]), "=&v"(r[2][0][0]), "=&v"(r[2][0][1]), "=&v"(r[3][0][0]), "=&v"(r[3][0][1])
+            : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "n"(HI)
+            : "memory");
+    } else if constexpr (BLOCKS == 4 && STEPS == 2) {
+        asm volatile(
+            "ds_read_b64_tr_b16 %0, %16\n"
+            "ds_read_b64_tr_b16 %1, %16 offset:%20\n"
+            "ds_read_b64_tr_b16 %2, %16 offset:%21\n"
+            "ds_read_b64_tr_b16 %3, %16 offset:%22\n"
+            "ds_read_b64_tr_b16 %4, %17\n"
+            "ds_read_b64_tr_b16 %5, %17 offset:%20\n"
+            "ds_read_b64_tr_b16 %6, %17 offset:%21\n"
+            "ds_read_b64_tr_b16 %7, %17 offset:%22\n"
+            "ds_read_b64_tr_b16 %8, %18\n"
+            "ds_read_b64_tr_b16 %9, %18 offset:%20\n"
+            "ds_read_b64_tr_b16 %10, %18 offset:%21\n"
+            "ds_read_b64_tr_b16 %11, %18 offset:%22\n"
+            "ds_read_b64_tr_b16 %12, %19\n"
+            "ds_read_b64_tr_b16 %13, %19 offset:%20\n"
+            "ds_read_b64_tr_b16 %14, %19 offset:%21\n"
+            "ds_read_b64_tr_b16 %15, %19 offset:%22\n"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(r[0][0][0]), "=&v"(r[0][0][1]), "=&v"(r[0][1][0]), "=&v"(r[0][1][1]), "=&v"(r[1][0][0]), "=&v"(r[1][0][1]), "=&v"(r[1][1][0]), "=&v"(r[1][1][1]), "=&v"(r[2][0][0]), "=&v"(r[2][0][1]), "=&v"(r[2][1][0]), "=&v"(r[2][1][1]), "=&v"(r[3][0][0]), "=&v"(r[3][0][1]), "=&v"(r[3][1][0]), "=&v"(r[3][1][1])
+            : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "n"(HI), "n"(NEXT), "n"(NEXT + HI)
+            : "memory");
+    }
+#pragma unroll
+    for (int b = 0; b < BLOCKS; ++b)
+#pragma unroll
+        for (int q = 0; q < STEPS; ++q)
+            f[b][q] = uintx4{r[b][q][0][0], r[b][q][0][1], r[b][q][1][0], r[b][q][1][1]};
+}
+
+// The LDS address of a pointer into shared memory.
+__device__ __forceinline__ unsigned lds_address(const unsigned char *p) {
+    return (unsigned)(unsigned long long)(
+        const __attribute__((address_space(3))) unsigned char *)p;
+}
+
 // Calls f with the constants 0 .. N-1.
 template <class F, int... I>
 __device__ __forceinline__ void each_of(std::integer_sequence<int, I...>, F &&f) {
@@ -268,6 +353,38 @@ __device__ __forceinline__ void finish_run(const Prod &p, int m, int n, const fl
             }
         }
     }
+}
+
+// The epilogue of a wave's 16 XB x 16 YB sums at (m0, n0), in MFMA layout:
+// sum(y, x) holds, in lane (i, g), row 16 x + i and columns 16 y + 4g .. +3.
+// They pass through `box` (LDS of this wave alone, 16 XB rows of 16 YB floats)
+// so that a lane then has eight adjacent columns, 16 bytes of a 16-bit result,
+// and neighbouring lanes neighbouring ones; the rows' 16-byte chunks are
+// swizzled against bank conflicts.  The loop is not unrolled: unrolled it takes
+// the same time and several times the code.
+template <int DT, int XB, int YB, class F>
+__device__ __forceinline__ void finish_wave(const Prod &p, int m0, int n0, int lane, float *box,
+                                            F &&sum) {
+    constexpr int CH = 4 * YB, LR = CH / 2;   // chunks per row, lanes per row
+    static_assert(CH == 8 || CH == 16, "rows of 32 or 64 columns");
+    auto swz = [](int row) { return CH == 16 ? row & 15 : (row >> 1) & 7; };
+    const int i = lane & 15, g = lane >> 4;
+    floatx4 *b4 = reinterpret_cast<floatx4 *>(box);
+    each<XB * YB>([&](auto j) __attribute__((always_inline)) {
+        constexpr int x = j / YB, y = j % YB;
+        const int row = 16 * x + i;
+        b4[row * CH + ((4 * y + g) ^ swz(row))] = sum(std::integral_constant<int, y>{},
+                                                      std::integral_constant<int, x>{});
+    });
+    with_act(p.act, [&](auto tag) __attribute__((always_inline)) {
+#pragma unroll 1
+        for (int r = lane / LR; r < 16 * XB; r += 64 / LR) {
+            const int q = lane % LR;
+            const floatx4 u = b4[r * CH + ((2 * q) ^ swz(r))], w = b4[r * CH + ((2 * q + 1) ^ swz(r))];
+            const float v[8] = {u[0], u[1], u[2], u[3], w[0], w[1], w[2], w[3]};
+            if (m0 + r < p.M) finish_run<DT, decltype(tag)::value>(p, m0 + r, n0 + 8 * q, v);
+        }
+    });
 }
 
 // Partial sums that another workgroup adds up are stored and loaded as
