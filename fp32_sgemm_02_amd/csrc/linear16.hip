@@ -326,6 +326,7 @@ bool direct_ok(const void *q, long long ld, int row_len, int bt, int mc) {
 
 struct Plan16 {
     int bm, bn, slices, per;
+    bool brief;   // one or two stages: a ring of two, so that more tiles share a CU
     bool big;   // linear16_big.hip
 };
 
@@ -348,6 +349,7 @@ Plan16 plan16(const Prod &p) {
         if (s > 32) s = 32;
         if (s < 1) s = 1;
     }
+    q.brief = stages <= 2;
     q.per = (stages + s - 1) / s;
     if (q.per < 1) q.per = 1;
     q.slices = stages ? (stages + q.per - 1) / q.per : 1;
@@ -356,16 +358,17 @@ Plan16 plan16(const Prod &p) {
 
 template <int DT, int BM, int BN, int WM, int WN, int NBUF, int KG, int AMC, int BMC>
 hipError_t launch_tile(const Prod &p, const Grid16 &gr, bool ad, bool bd, hipStream_t stream) {
+    // (operands that are not loaded directly have two stages whatever NBUF is)
     constexpr int NT = 64 * (BM / WM) * (BN / WN) * KG;
     const dim3 grid(gr.tiles_m * gr.tiles_n, gr.slices);
     if (ad && bd)
         hipLaunchKernelGGL((prod16_kernel<DT, BM, BN, WM, WN, NBUF, KG, AMC, BMC, true, true>), grid,
                            dim3(NT), 0, stream, p, gr);
     else if (ad && BMC)   // the backward products: G is laid out for direct loads, B may not be
-        hipLaunchKernelGGL((prod16_kernel<DT, BM, BN, WM, WN, NBUF, KG, AMC, BMC, BMC != 0, false>), grid,
+        hipLaunchKernelGGL((prod16_kernel<DT, BM, BN, WM, WN, 2, KG, AMC, BMC, BMC != 0, false>), grid,
                            dim3(NT), 0, stream, p, gr);
     else
-        hipLaunchKernelGGL((prod16_kernel<DT, BM, BN, WM, WN, NBUF, KG, AMC, BMC, false, false>), grid,
+        hipLaunchKernelGGL((prod16_kernel<DT, BM, BN, WM, WN, 2, KG, AMC, BMC, false, false>), grid,
                            dim3(NT), 0, stream, p, gr);
     return hipGetLastError();
 }
@@ -392,8 +395,11 @@ hipError_t launch_dt(Prod p, const Workspace &ws, hipStream_t stream) {
     gr.count = ws.counters;
     const bool ad = direct_ok(p.A, p.lda, p.a_pad ? 0 : p.a_mc ? p.M : p.K, q.bm, p.a_mc);
     const bool bd = direct_ok(p.B, p.ldb, p.b_mc ? p.N : p.K, q.bn, p.b_mc);
-    if (q.bm == 128) return launch_layout<DT, 128, 128, 64, 64, 4, 2>(p, gr, ad, bd, stream);
-    return launch_layout<DT, 64, 64, 32, 32, 4, 2>(p, gr, ad, bd, stream);
+    if (q.bm == 128)
+        return q.brief ? launch_layout<DT, 128, 128, 64, 64, 2, 2>(p, gr, ad, bd, stream)
+                       : launch_layout<DT, 128, 128, 64, 64, 4, 2>(p, gr, ad, bd, stream);
+    return q.brief ? launch_layout<DT, 64, 64, 32, 32, 2, 2>(p, gr, ad, bd, stream)
+                   : launch_layout<DT, 64, 64, 32, 32, 4, 2>(p, gr, ad, bd, stream);
 }
 
 }  // namespace

@@ -12,6 +12,7 @@ namespace {
 
 struct RowsGrid {
     int strips, slices, kslice;   // column strips, k slices, k per slice
+    int width;                    // columns per strip
     float *part;                  // slices x strips x the strip's accumulators
     unsigned *count;              // one arrival counter per strip, zero between launches
 };
@@ -86,6 +87,87 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(Prod p, RowsGrid gr) {
     with_act(p.act, [&](auto tag) {
         finish_run<DT, decltype(tag)::value>(p, m, n0 + 4 * g, v);
     });
+}
+
+// Strips of `width` rows of W (at most 16 RB), staged (stream_rows.hpp), the
+// eight waves taking the stages of a slice in turn and meeting in LDS.
+template <int DT, int RB, int TB>
+__global__ void __launch_bounds__(512) rows_staged_kernel(Prod p, RowsGrid gr) {
+#ifdef __HIP_DEVICE_COMPILE__   // the host pass needs the launch stub only
+    using T = typename Type<DT>::T;
+    constexpr int NW = 8;
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[NW * 2 * kStageBytes];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int i = lane & 15, g = lane >> 4;
+    const int strip = blockIdx.x % gr.strips, slice = blockIdx.x / gr.strips;
+    const int n0 = strip * gr.width, rows = min(gr.width, p.N - n0);
+    int xoff[TB];
+#pragma unroll
+    for (int t = 0; t < TB; ++t) xoff[t] = min(16 * t + i, p.M - 1) * (int)p.lda * (int)sizeof(T);
+    const int ks = slice * gr.kslice, ke = min(ks + gr.kslice, p.K);
+    floatx4 acc[RB][TB];
+#pragma unroll
+    for (int r = 0; r < RB; ++r)
+#pragma unroll
+        for (int t = 0; t < TB; ++t) acc[r][t] = floatx4{0.f, 0.f, 0.f, 0.f};
+    staged_dot<DT, RB, TB>(static_cast<const T *>(p.B) + (long long)n0 * p.ldb, p.ldb, rows,
+                           static_cast<const T *>(p.A), xoff, ks, ke, wave, NW,
+                           smem + wave * 2 * kStageBytes, lane, acc);
+    // the ring is this wave's own up to here; now every wave leaves its sums
+    static_assert(NW * RB * TB * 1024 <= (int)sizeof(smem), "the waves' sums fit the ring");
+    floatx4 *red = reinterpret_cast<floatx4 *>(smem);
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < RB; ++r)
+#pragma unroll
+        for (int t = 0; t < TB; ++t) red[((r * TB + t) * NW + wave) * 64 + lane] = acc[r][t];
+    __syncthreads();
+    // wave v finishes blocks v, v + 8, ... of the strip's RB x TB
+    auto sum_of = [&](int b) {
+        floatx4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int z = 0; z < NW; ++z) {
+            const floatx4 v = red[(b * NW + z) * 64 + lane];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[e] += v[e];
+        }
+        return s;
+    };
+    auto finish = [&](int b, const floatx4 &s) {
+        const int m = 16 * (b % TB) + i, c = 16 * (b / TB) + 4 * g;
+        if (m >= p.M || c >= rows) return;
+        const float v[4] = {s[0], s[1], s[2], s[3]};
+        with_act(p.act, [&](auto tag) { finish_run<DT, decltype(tag)::value>(p, m, n0 + c, v); });
+    };
+    if (gr.slices == 1) {
+        for (int b = wave; b < RB * TB; b += NW) finish(b, sum_of(b));
+        return;
+    }
+    auto at = [&](int s, int b) {
+        return gr.part + ((((long long)s * gr.strips + strip) * (RB * TB) + b) * 64 + lane) * 4;
+    };
+    for (int b = wave; b < RB * TB; b += NW) store_partial(at(slice, b), sum_of(b));
+    __syncthreads();   // red is read: its first word takes the flag
+    if (!arrive_last(gr.count + strip, gr.slices, reinterpret_cast<int *>(smem))) return;
+    for (int b = wave; b < RB * TB; b += NW) {
+        floatx4 sum = {0.f, 0.f, 0.f, 0.f};
+        for (int s = 0; s < gr.slices; s += 8) {
+            floatx4 v[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                v[q] = s + q < gr.slices ? load_partial(at(s + q, b)) : floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (s + q < gr.slices)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sum[e] += v[q][e];
+        }
+        finish(b, sum);
+    }
+    if (tid == 0)
+        __hip_atomic_store(gr.count + strip, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#endif
 }
 
 // dX = G W: a strip of 16 V columns of W per workgroup (V values to 16
@@ -221,37 +303,65 @@ __global__ void __launch_bounds__(kThreads) cols_kernel(Prod p, RowsGrid gr) {
 }
 
 struct PlanRows {
-    int strips, slices, kslice, tb, acc;
+    int strips, slices, kslice, width, tb, rb, acc;
+    bool staged;
 };
 
+constexpr int kCUs = 256;
+
 PlanRows plan_rows(int dtype, const Prod &p) {
-    const int v = dtype == SGEMM_DTYPE_F32 ? 4 : 8, step = 4 * v;
-    PlanRows q;
+    const int elem = dtype == SGEMM_DTYPE_F32 ? 4 : 2, v = 16 / elem, step = 4 * v;
+    PlanRows q{};
     q.tb = p.M > 32 ? 4 : p.M > 16 ? 2 : 1;
-    const int cols = p.b_mc ? 16 * v : 16;
-    q.acc = (p.b_mc ? v : 1) * q.tb;   // 16-byte accumulators per lane of a strip
-    q.strips = (p.N + cols - 1) / cols;
-    // split k until two workgroups per CU are in flight, each wave keeping
-    // four steps at least
-    int s = 1;
-    if (q.strips < 256 && q.strips <= kWorkspaceCounters) {
-        s = (512 + q.strips - 1) / q.strips;
-        const int most = p.K / (kWaves * 4 * step);
-        if (s > most) s = most;
-        if (s > 64) s = 64;
-        if (s < 1) s = 1;
+    q.staged = !p.b_mc && stage_ok(p.B, p.ldb, p.K, elem) && stage_ok(p.A, p.lda, p.K, elem);
+    int s = 1, unit = step;
+    if (q.staged) {
+        // one strip per CU where N reaches for it: as wide as it has to be, up
+        // to 64 columns (then several strips per CU)
+        const int rounds = (p.N + 64 * kCUs - 1) / (64 * kCUs);
+        q.width = ((p.N + rounds * kCUs - 1) / (rounds * kCUs) + 3) / 4 * 4;
+        if (q.width < 16) q.width = 16;
+        q.rb = q.width > 32 ? 4 : q.width > 16 ? 2 : 1;
+        q.acc = q.rb * q.tb;
+        q.strips = (p.N + q.width - 1) / q.width;
+        unit = 512 / q.rb / elem;
+        // a slice keeps one stage for every wave
+        if (q.strips <= kCUs / 2) {
+            s = kCUs / q.strips;
+            const int most = p.K / (8 * unit);
+            if (s > most) s = most;
+        }
+    } else {
+        q.width = p.b_mc ? 16 * v : 16;
+        q.acc = (p.b_mc ? v : 1) * q.tb;   // 16-byte accumulators per lane of a strip
+        q.strips = (p.N + q.width - 1) / q.width;
+        // split k until two workgroups per CU are in flight, each wave keeping
+        // four steps at least
+        if (q.strips < kCUs && q.strips <= kWorkspaceCounters) {
+            s = (2 * kCUs + q.strips - 1) / q.strips;
+            const int most = p.K / (kWaves * 4 * step);
+            if (s > most) s = most;
+            if (s > 64) s = 64;
+        }
     }
-    q.kslice = ((p.K + s - 1) / s + step - 1) / step * step;
-    if (q.kslice < step) q.kslice = step;
+    if (s < 1) s = 1;
+    q.kslice = ((p.K + s - 1) / s + unit - 1) / unit * unit;
+    if (q.kslice < unit) q.kslice = unit;
     q.slices = (p.K + q.kslice - 1) / q.kslice;
     if (q.slices < 1) q.slices = 1;
     return q;
 }
 
 template <int DT, int TB>
-hipError_t launch_tb(const Prod &p, const RowsGrid &gr, hipStream_t stream) {
+hipError_t launch_tb(const Prod &p, const PlanRows &q, const RowsGrid &gr, hipStream_t stream) {
     const dim3 grid((unsigned)gr.strips * gr.slices), block(kThreads);
-    if (!p.b_mc)
+    if (q.staged && q.rb == 1)
+        hipLaunchKernelGGL((rows_staged_kernel<DT, 1, TB>), grid, dim3(512), 0, stream, p, gr);
+    else if (q.staged && q.rb == 2)
+        hipLaunchKernelGGL((rows_staged_kernel<DT, 2, TB>), grid, dim3(512), 0, stream, p, gr);
+    else if (q.staged)
+        hipLaunchKernelGGL((rows_staged_kernel<DT, 4, TB>), grid, dim3(512), 0, stream, p, gr);
+    else if (!p.b_mc)
         hipLaunchKernelGGL((rows_kernel<DT, TB, TB == 1 ? 8 : 4>), grid, block, 0, stream, p, gr);
     else if (DT != SGEMM_DTYPE_F32 && p.lo)
         hipLaunchKernelGGL((cols_kernel<DT, TB, DT != SGEMM_DTYPE_F32>), grid, block, 0, stream, p,
@@ -265,11 +375,12 @@ template <int DT>
 hipError_t launch_dt(Prod p, const Workspace &ws, hipStream_t stream) {
     const PlanRows q = plan_rows(DT, p);
     p.cvec = epilogue_vec(p, (int)sizeof(typename Type<DT>::T));
-    const RowsGrid gr{q.strips, q.slices, q.kslice, static_cast<float *>(ws.ptr), ws.counters};
+    const RowsGrid gr{q.strips, q.slices, q.kslice, q.width, static_cast<float *>(ws.ptr),
+                      ws.counters};
     switch (q.tb) {
-    case 1: return launch_tb<DT, 1>(p, gr, stream);
-    case 2: return launch_tb<DT, 2>(p, gr, stream);
-    default: return launch_tb<DT, 4>(p, gr, stream);
+    case 1: return launch_tb<DT, 1>(p, q, gr, stream);
+    case 2: return launch_tb<DT, 2>(p, q, gr, stream);
+    default: return launch_tb<DT, 4>(p, q, gr, stream);
     }
 }
 

@@ -1,6 +1,5 @@
 // stream_rows.hpp -- the inner loops of products with few rows, in which the
-// weights are streamed once from memory into registers (no LDS staging: every
-// weight value is used by one wave only, so a copy in LDS would be read once).
+// weights are streamed once from memory.
 //
 // A fragment is 16 bytes per lane: the 8 k values of one v_mfma_f32_16x16x32
 // (16-bit types) or the 4 k values of four v_mfma_f32_16x16x4 (fp32; step s
@@ -110,6 +109,107 @@ __device__ __forceinline__ void stream_dot(const typename Type<DT>::T *const (&w
         products(b);
         pipeline_fence();
     }
+}
+
+// ---- staged form ---------------------------------------------------------------
+// acc[r][t] += the products of 16 RB weight rows and 16 TB token rows, the weights
+// passing through a ring of two stages in LDS that belongs to this wave alone
+// (no barriers).  A direct load copies whole runs of 512 / RB bytes of a row,
+// where fragments loaded straight into registers take 64 bytes of each of 16
+// rows at a time: 16 x 14336 x 4096 bf16 FIG_STAGED.  A stage is 8 KB: KST
+// values of k of every row.  The waves of a workgroup take the stages in turn.
+// Needs rows of 16-byte chunks; what lies outside (rows past the end, chunks
+// past kend) reads as zero.
+//
+// Order of the loads of stage s: its token fragments, then the weights of stage
+// s + 1; with all but the last 8 loads waited for, both operands of stage s are
+// there and the weights of stage s + 1 are in flight.
+constexpr int kStageBytes = 8192;
+template <int DT, int RB>
+constexpr int kStageK = 512 / RB / (int)sizeof(typename Type<DT>::T);   // KST
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(const void *p) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, 0x7fffffff, 0x00020000);
+}
+
+// Whether a matrix's rows serve the staged form: whole 16-byte chunks, and 64
+// rows within 31 bits of byte offsets.
+inline bool stage_ok(const void *p, long long ld, int len, int elem) {
+    return rows16(p, ld, elem) && (long long)len * elem % 16 == 0 && 64 * ld * elem < 0x7fff0000LL;
+}
+
+// w: row 0 of the strip, `rows` of them inside; x: token 0, off[t]: byte offset
+// of this lane's row of token block t from x; both at k = 0.  The wave takes
+// the stages first, first + step, ... below kend / KST.  ring: 2 * kStageBytes.
+template <int DT, int RB, int TB>
+__device__ __forceinline__ void staged_dot(const typename Type<DT>::T *w, long long ldw, int rows,
+                                           const typename Type<DT>::T *x, const int (&xoff)[TB],
+                                           int k0, int kend, int first, int step,
+                                           unsigned char *ring, int lane, floatx4 (&acc)[RB][TB]) {
+    using T = typename Type<DT>::T;
+    constexpr int V = Step<DT>::V, KST = kStageK<DT, RB>, ROW = 512 / RB, CH = ROW / 16;
+    constexpr int STEPS = CH / 4, E = (int)sizeof(T);
+    constexpr int kOut = (int)0x80000000u;
+    typedef __attribute__((address_space(3))) void lds_void;
+    const int i = lane & 15, g = lane >> 4;
+    // 16 lanes read one chunk of 16 rows: their slots differ mod 256 bytes
+    auto swz = [](int r) { return CH == 8 ? (r >> 1) & 7 : r & 15; };
+    int off[8], kk[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int q = j * 64 + lane, r = q / CH, c = (q % CH) ^ swz(r);
+        kk[j] = c * V;
+        off[j] = r < rows ? r * (int)ldw * E + c * 16 : kOut;
+    }
+    const int stages = (kend - k0 + KST - 1) / KST;
+    auto load_w = [&](int s, int slot) {
+        const int k = k0 + s * KST, krem = s < stages ? kend - k : 0;
+        const __amdgpu_buffer_rsrc_t b = row_buffer(w + k);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                b, (lds_void *)(ring + slot * kStageBytes + j * 1024), 16,
+                kk[j] < krem ? off[j] : kOut, 0, 0, 0);
+    };
+    if (first >= stages) return;
+    load_w(first, 0);
+    int slot = 0;
+    for (int s = first; s < stages; s += step, slot ^= 1) {
+        const int k = k0 + s * KST;
+        const __amdgpu_buffer_rsrc_t xb = row_buffer(x + k);
+        uintx4 fx[STEPS][TB];
+#pragma unroll
+        for (int u = 0; u < STEPS; ++u)
+#pragma unroll
+            for (int t = 0; t < TB; ++t) {
+                const int kc = V * (4 * u + g);
+                fx[u][t] = __builtin_bit_cast(
+                    uintx4, __builtin_amdgcn_raw_buffer_load_b128(
+                                xb, k + kc < kend ? xoff[t] + kc * E : kOut, 0, 0));
+            }
+        pipeline_fence();
+        load_w(s + step, slot ^ 1);
+        pipeline_fence();
+        __builtin_amdgcn_s_waitcnt(8 | (7 << 4) | (15 << 8));   // all but the last 8 loads
+        pipeline_fence();
+        const unsigned char *img = ring + slot * kStageBytes;
+#pragma unroll
+        for (int u = 0; u < STEPS; ++u)
+#pragma unroll
+            for (int r = 0; r < RB; ++r) {
+                const int row = 16 * r + i;
+                const uintx4 fw = *reinterpret_cast<const uintx4 *>(
+                    img + row * ROW + (((4 * u + g) ^ swz(row)) << 4));
+#pragma unroll
+                for (int t = 0; t < TB; ++t) acc[r][t] = mfma_step<DT>(fw, fx[u][t], acc[r][t]);
+            }
+        // the reads of this stage are done before its place is loaded again
+        pipeline_fence();
+        __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4));
+        pipeline_fence();
+    }
+    __builtin_amdgcn_s_waitcnt((7 << 4) | (15 << 8));   // no load left in flight
+    pipeline_fence();
 }
 
 }  // namespace sg
