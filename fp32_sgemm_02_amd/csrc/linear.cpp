@@ -254,7 +254,7 @@ int sgemm_moe(int dtype, int T, int D, int F, int E, int top_k, int gated, int r
     if (!known(dtype)) return bad(1);
     const int elem = elem_of(dtype);
     if (T < 0 || T > kMoeTokens) return bad(2);
-    if (D < 1 || D > 16 * (kWorkspaceCounters - kMoeTokens)) return bad(3);
+    if (D < 1 || D > kMoeWidth) return bad(3);
     if (F < 1 || F > (1 << 20)) return bad(4);
     if (E < 1 || E > kMoeExperts) return bad(5);
     if (top_k < 1 || top_k > kMoeChoices || top_k > E) return bad(6);

@@ -73,6 +73,7 @@ hipError_t launch_grad(int dtype, int M, int N, const void *dY, long long lddy, 
 
 // A mixture-of-experts layer for few tokens (moe.hip); see sgemm_moe.
 constexpr int kMoeTokens = 64, kMoeExperts = 512, kMoeChoices = 16;
+constexpr int kMoeWidth = 64512;   // an arrival counter for every 32 columns of Y
 struct Moe {
     int T, D, F, E, k;
     int gated, renorm, act;
@@ -97,7 +98,7 @@ hipError_t launch_finish32(int M, int N, const float *Z, long long ldz, int act,
                            long long ldr, float *Y, long long ldy, hipStream_t stream);
 
 // Whether rows of an array take 16-byte accesses.
-inline bool rows16(const void *q, long long ld, int elem) {
+__host__ __device__ inline bool rows16(const void *q, long long ld, int elem) {
     return reinterpret_cast<unsigned long long>(q) % 16 == 0 && ld * elem % 16 == 0;
 }
 inline int epilogue_vec(const Prod &p, int elem) {

@@ -111,7 +111,8 @@ __global__ void __launch_bounds__(512) rows_staged_kernel(Prod p, RowsGrid gr) {
     for (int r = 0; r < RB; ++r)
 #pragma unroll
         for (int t = 0; t < TB; ++t) acc[r][t] = floatx4{0.f, 0.f, 0.f, 0.f};
-    staged_dot<DT, RB, TB>(static_cast<const T *>(p.B) + (long long)n0 * p.ldb, p.ldb, rows,
+    staged_dot<DT, RB, TB>(static_cast<const T *>(p.B) + (long long)n0 * p.ldb,
+                           [&](int r) { return r < rows ? r * (int)p.ldb * (int)sizeof(T) : kOut; },
                            static_cast<const T *>(p.A), xoff, ks, ke, wave, NW,
                            smem + wave * 2 * kStageBytes, lane, acc);
     // the ring is this wave's own up to here; now every wave leaves its sums
