@@ -64,21 +64,29 @@ __global__ void __launch_bounds__(kThreads) router_kernel(Moe m, MoeWs s) {
             w[q] = static_cast<const T *>(m.Wr) + (long long)min(e0 + q, m.E - 1) * m.ldwr;
             sum[q] = 0.0;
         }
-#pragma unroll 2
-        for (int d = lane * V; d < m.D; d += 64 * V) {
-            uintx4 b[EPW];
-            const uintx4 a = load_frag<DT>(x + d, m.D - d);
+        // U chunks' loads in flight: a few tokens' logits wait for memory only
+        constexpr int U = EPW == 1 ? 4 : 2;
+        for (int d0 = lane * V; d0 < m.D; d0 += U * 64 * V) {
+            uintx4 a[U], b[U][EPW];
 #pragma unroll
-            for (int q = 0; q < EPW; ++q) b[q] = load_frag<DT>(w[q] + d, m.D - d);
-            T av[V];
-            __builtin_memcpy(av, &a, 16);
+            for (int u = 0; u < U; ++u) {
+                const int d = d0 + u * 64 * V;
+                a[u] = load_frag<DT>(x + d, m.D - d);
 #pragma unroll
-            for (int q = 0; q < EPW; ++q) {
-                T bv[V];
-                __builtin_memcpy(bv, &b[q], 16);
+                for (int q = 0; q < EPW; ++q) b[u][q] = load_frag<DT>(w[q] + d, m.D - d);
+            }
 #pragma unroll
-                for (int z = 0; z < V; ++z)
-                    sum[q] = fma((double)Ty::load(av[z]), (double)Ty::load(bv[z]), sum[q]);
+            for (int u = 0; u < U; ++u) {
+                T av[V];
+                __builtin_memcpy(av, &a[u], 16);
+#pragma unroll
+                for (int q = 0; q < EPW; ++q) {
+                    T bv[V];
+                    __builtin_memcpy(bv, &b[u][q], 16);
+#pragma unroll
+                    for (int z = 0; z < V; ++z)
+                        sum[q] = fma((double)Ty::load(av[z]), (double)Ty::load(bv[z]), sum[q]);
+                }
             }
         }
 #pragma unroll
@@ -109,6 +117,7 @@ __global__ void __launch_bounds__(kThreads) router_kernel(Moe m, MoeWs s) {
     for (int e = tid; e < m.E; e += kThreads) {
         const double v = lg[e];
         int rank = 0;
+#pragma unroll 8
         for (int o = 0; o < m.E; ++o) rank += lg[o] > v || (lg[o] == v && o < e);
         if (rank < m.k) {
             best[rank] = v;
@@ -117,27 +126,29 @@ __global__ void __launch_bounds__(kThreads) router_kernel(Moe m, MoeWs s) {
     }
     __syncthreads();
     const double top = best[0];
-    double all = 0.0;
-    if (m.renorm) {
-        for (int j = 0; j < m.k; ++j) all += exp(best[j] - top);   // the same in every thread
-    } else {
+    const double mine = lane < m.k ? exp(best[lane] - top) : 0.0;
+    double all = mine;
+    if (!m.renorm) {
+        all = 0.0;
         for (int e = tid; e < m.E; e += kThreads) all += exp(lg[e] - top);
+    }
 #pragma unroll
-        for (int o = 32; o >= 1; o /= 2) all += __shfl_xor(all, o);
+    for (int o = 32; o >= 1; o /= 2) all += __shfl_xor(all, o);
+    if (!m.renorm) {   // the waves hold different experts' terms
         if (lane == 0) red[wave] = all;
         __syncthreads();
         all = ((red[0] + red[1]) + red[2]) + red[3];
     }
     if (tid < m.k) {
-        const float w = nan ? __builtin_nanf("") : (float)(exp(best[tid] - top) / all);
+        const float w = nan ? __builtin_nanf("") : (float)(mine / all);
         const int id = best_id[tid];
         __hip_atomic_store(s.ids + t * m.k + tid, id, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         s.w[t * m.k + tid] = w;
         if (m.ids) m.ids[t * m.k + tid] = id;
         if (m.weights) m.weights[t * m.k + tid] = w;
     }
-    if (!arrive_last(s.chosen, m.T, &last)) return;
-    if (tid == 0) __hip_atomic_store(s.chosen, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (m.T > 1 && !arrive_last(s.chosen, m.T, &last)) return;
+    if (m.T > 1 && tid == 0) __hip_atomic_store(s.chosen, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 
     // the choices by expert, ascending: a token chooses an expert once at most,
     // so an expert's choices are a mask of tokens
@@ -146,13 +157,14 @@ __global__ void __launch_bounds__(kThreads) router_kernel(Moe m, MoeWs s) {
     Routing *r = s.routing;
     for (int e = tid; e < kMoeExperts; e += kThreads) users[e] = 0;
     __syncthreads();
-    int mine[kPairs / kThreads];
+    int chosen[kPairs / kThreads];
 #pragma unroll
     for (int q = 0; q < kPairs / kThreads; ++q) {
         const int p = q * kThreads + tid;
         if (p >= P) break;
-        mine[q] = __hip_atomic_load(s.ids + p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        atomicOr(&users[mine[q]], 1ull << (p / m.k));
+        chosen[q] = m.T == 1 ? best_id[p]
+                           : __hip_atomic_load(s.ids + p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        atomicOr(&users[chosen[q]], 1ull << (p / m.k));
     }
     __syncthreads();
     if (wave == 0) {
@@ -183,8 +195,8 @@ __global__ void __launch_bounds__(kThreads) router_kernel(Moe m, MoeWs s) {
     for (int q = 0; q < kPairs / kThreads; ++q) {
         const int p = q * kThreads + tid;
         if (p >= P) break;
-        const unsigned long long earlier = users[mine[q]] & ((1ull << (p / m.k)) - 1);
-        r->list[first_of[mine[q]] + __popcll(earlier)] = p;
+        const unsigned long long earlier = users[chosen[q]] & ((1ull << (p / m.k)) - 1);
+        r->list[first_of[chosen[q]] + __popcll(earlier)] = p;
     }
 }
 
