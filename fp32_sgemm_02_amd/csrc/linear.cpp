@@ -119,31 +119,31 @@ int run_backward(int dtype, const Backward &b, hipStream_t stream) {
     const bool want_db = b.db && b.N > 0;
     const bool few = b.M <= kFewRows;
     // G is dY itself without an activation, as long as the 16-bit tiles can
-    // load its rows directly
+    // load its rows directly (the few-rows kernels load any)
     const bool g_is_dy = b.act == SGEMM_ACT_NONE &&
-                         (f32 || (rows16(b.dY, b.lddy, elem) && b.N % v == 0));
+                         (f32 || few || (rows16(b.dY, b.lddy, elem) && b.N % v == 0));
     const bool make_g = !g_is_dy && (want_dx || want_dw) && b.M > 0 && b.N > 0;
     // few rows: both products are bound by W and dW, so G is kept in two parts
     // (as exact as fp32) at no cost; otherwise its rounding adds an error of
-    // the size of the results' own rounding
-    const bool two = make_g && few && !f32 && b.act != SGEMM_ACT_NONE;
+    // the size of the results' own rounding (ReLU's slope is 0 or 1: nothing to
+    // round)
+    const bool two = make_g && few && !f32 && b.act != SGEMM_ACT_NONE && b.act != SGEMM_ACT_RELU;
     const long long ldg = make_g ? (long long)round_up(b.N, v) : b.lddy;
     const size_t g_bytes =
-        make_g ? round_up((size_t)(two ? 2 * kFewRows : b.M) * ldg * elem, 256) : 0;
+        make_g ? round_up((size_t)(two ? 2 : 1) * b.M * ldg * elem, 256) : 0;
 
     Prod dx{b.M, b.K, b.N, b.dY, ldg, b.W, b.ldw, b.dX, b.lddx};
     dx.b_mc = 1;
     Prod dw{b.N, b.K, b.M, b.dY, ldg, b.X, b.ldx, b.dW, b.lddw};
     dw.a_mc = dw.b_mc = 1;
     dx.a_pad = dw.a_pad = make_g;
-    dw.fold = two;
-    const bool dx_ours = want_dx && (!f32 || few), dw_ours = want_dw && !f32;
+    const bool dx_ours = want_dx && (!f32 || few), dw_ours = want_dw && (!f32 || few);
     size_t scratch = want_db ? grad_workspace(dtype, b.M, b.N) : 0;
     if (dx_ours) {
         const size_t s = product_workspace(dtype, dx, few);
         if (s > scratch) scratch = s;
     }
-    if (dw_ours) {
+    if (dw_ours && !few) {
         const size_t s = product_workspace(dtype, dw, false);
         if (s > scratch) scratch = s;
     }
@@ -151,14 +151,14 @@ int run_backward(int dtype, const Backward &b, hipStream_t stream) {
         const Workspace rest = ws.ptr ? part_of(ws, g_bytes) : ws;
         if (make_g || want_db) {
             unsigned char *G = make_g ? static_cast<unsigned char *>(ws.ptr) : nullptr;
-            void *lo = two ? G + (size_t)kFewRows * ldg * elem : nullptr;
+            void *lo = two ? G + (size_t)b.M * ldg * elem : nullptr;
             const hipError_t e =
                 launch_grad(dtype, b.M, b.N, b.dY, b.lddy, b.Z, b.ldz, b.act, G, lo, ldg,
                             want_db ? b.db : nullptr, static_cast<float *>(rest.ptr),
                             rest.counters, stream);
             if (e != hipSuccess) return to_status(e);
             if (make_g) dx.A = dw.A = G;
-            dx.lo = lo;
+            dx.lo = dw.lo = lo;
         }
         if (want_dx) {
             int st;
@@ -171,6 +171,7 @@ int run_backward(int dtype, const Backward &b, hipStream_t stream) {
             if (st != 0) return st;
         }
         if (want_dw) {
+            if (few) return to_status(launch_outer(dtype, dw, stream));
             if (dw_ours) return to_status(launch_product(dtype, dw, false, rest, stream));
             return sgemm_op(1, 0, b.N, b.K, b.M, 1.f, static_cast<const float *>(dw.A), (int)ldg,
                             static_cast<const float *>(b.X), b.ldx, 0.f,

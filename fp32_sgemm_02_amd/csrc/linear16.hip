@@ -180,14 +180,23 @@ __device__ __forceinline__ bool join_slices(const Grid16 &gr, int tile, int tile
     for (int j = 0; j < NB * MB; ++j) store_partial(at(slice, j), acc[j / MB][j % MB]);
     if (!arrive_last(gr.count + tile, gr.slices, last)) return false;
 #pragma unroll
-    for (int j = 0; j < NB * MB; ++j) acc[j / MB][j % MB] = load_partial(at(0, j));
-    for (int s = 1; s < gr.slices; ++s)
+    for (int j = 0; j < NB * MB; ++j) acc[j / MB][j % MB] = floatx4{0.f, 0.f, 0.f, 0.f};
+    // two slices' loads in flight at a time
+    for (int s = 0; s < gr.slices; s += 2) {
+        floatx4 v[2][NB * MB];
 #pragma unroll
-        for (int j = 0; j < NB * MB; ++j) {
-            const floatx4 v = load_partial(at(s, j));
+        for (int q = 0; q < 2; ++q)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[j / MB][j % MB][e] += v[e];
-        }
+            for (int j = 0; j < NB * MB; ++j)
+                v[q][j] = s + q < gr.slices ? load_partial(at(s + q, j)) : floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            if (s + q < gr.slices)
+#pragma unroll
+                for (int j = 0; j < NB * MB; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[j / MB][j % MB][e] += v[q][j][e];
+    }
     if (tid == 0) __hip_atomic_store(gr.count + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     return true;
 }
@@ -223,7 +232,7 @@ prod16_kernel(Prod p, Grid16 gr) {
     const int tile = xcd_remap(blockIdx.x, tiles);
     tile_coords(tile, gr.tiles_m, gr.tiles_n, gr.group_m, tm, tn);
     const int m0 = tm * BM, n0 = tn * BN;
-    const int stages = p.fold ? 2 : (p.K + kBK - 1) / kBK;
+    const int stages = (p.K + kBK - 1) / kBK;
     const int t0 = slice * gr.per, t1 = min(t0 + gr.per, stages);
 
     OpA a;
@@ -239,9 +248,9 @@ prod16_kernel(Prod p, Grid16 gr) {
 
     auto issue = [&](int t, unsigned char *img) {
         // stages past the slice's end read zeros
-        const int krem = t >= t1 ? 0 : p.fold ? p.K : p.K - t * kBK;
+        const int krem = t >= t1 ? 0 : p.K - t * kBK;
         a.issue(t, krem, img, wave);
-        b.issue(p.fold ? 0 : t, krem, img + OpA::BYTES, wave);
+        b.issue(t, krem, img + OpA::BYTES, wave);
     };
 #pragma unroll
     for (int q = 0; q < AHEAD; ++q) issue(t0 + q, smem[q]);
@@ -335,14 +344,14 @@ constexpr int kCUs = 256;
 Plan16 plan16(const Prod &p) {
     auto tiles = [&](int b) { return (long long)((p.M + b - 1) / b) * ((p.N + b - 1) / b); };
     Plan16 q{};
-    q.big = !p.fold && tiles(256) >= kCUs / 2 &&
+    q.big = tiles(256) >= kCUs / 2 &&
             direct_ok(p.A, p.lda, p.a_pad ? 0 : p.a_mc ? p.M : p.K, 256, p.a_mc) &&
             direct_ok(p.B, p.ldb, p.b_mc ? p.N : p.K, 256, p.b_mc);
     q.bm = q.bn = tiles(128) >= kCUs ? 128 : 64;
     const long long t = tiles(q.bm);
-    const int stages = p.fold ? 2 : (p.K + kBK - 1) / kBK;
+    const int stages = (p.K + kBK - 1) / kBK;
     int s = 1;
-    if (!p.fold && !q.big && t <= kCUs / 2) {
+    if (!q.big && t <= kCUs / 2) {
         s = (int)(kCUs / t);
         const int most = stages / 4;
         if (s > most) s = most;

@@ -4,8 +4,8 @@
 //
 // Memory-bound: dY and Z are read once and G written once, 16 bytes per lane
 // where the rows allow it, and the column sums are taken from the fp32 values
-// on the way.  A workgroup owns a block of columns (32 lanes of 16 bytes) and
-// a band of rows (8 row lanes); the bands' partial sums go to memory as
+// on the way.  A workgroup owns a block of columns (16 lanes of 16 bytes) and
+// a band of rows (16 row lanes); the bands' partial sums go to memory as
 // device-coherent stores and the workgroup of a column block that counts last
 // adds them in band order.
 #include "linear_internal.hpp"
@@ -14,6 +14,7 @@ namespace sg {
 namespace {
 
 constexpr int kF32 = SGEMM_DTYPE_F32;
+constexpr int kColLanes = 16, kRowLanes = 16;   // lanes of a workgroup
 
 struct GradArgs {
     int M, N;
@@ -31,10 +32,10 @@ template <int DT, int ACT>
 __global__ void __launch_bounds__(256) grad_kernel(GradArgs a) {
     using Ty = Type<DT>;
     using T = typename Ty::T;
-    constexpr int V = Ty::V, COLS = 32 * V;
-    __shared__ float red[8][COLS];
+    constexpr int V = Ty::V, COLS = kColLanes * V;
+    __shared__ float red[kRowLanes][COLS];
     __shared__ int last;
-    const int tid = threadIdx.x, cl = tid & 31, rl = tid >> 5;
+    const int tid = threadIdx.x, cl = tid % kColLanes, rl = tid / kColLanes;
     const int n0 = blockIdx.x * COLS, n = n0 + cl * V;
     const int r0 = blockIdx.y * a.band, r1 = min(r0 + a.band, a.M);
     const int cols = min(V, a.N - n);
@@ -42,8 +43,11 @@ __global__ void __launch_bounds__(256) grad_kernel(GradArgs a) {
 #pragma unroll
     for (int e = 0; e < V; ++e) sum[e] = 0.f;
     if (cols > 0) {
-        const bool vec = a.vec && cols == V;
-        for (int r = r0 + rl; r < r1; r += 8) {
+        // (the same for the whole block, so that the loads of several rows run
+        // together)
+        const bool vec = a.vec && (n0 + COLS <= a.N || a.N % V == 0);
+#pragma unroll 2
+        for (int r = r0 + rl; r < r1; r += kRowLanes) {
             const T *dy = static_cast<const T *>(a.dY) + (long long)r * a.lddy + n;
             const T *z = static_cast<const T *>(a.Z) + (long long)r * a.ldz + n;
             T *g = a.G ? static_cast<T *>(a.G) + (long long)r * a.ldg + n : nullptr;
@@ -84,7 +88,7 @@ __global__ void __launch_bounds__(256) grad_kernel(GradArgs a) {
     for (int c = tid; c < COLS && n0 + c < a.N; c += 256) {
         float s = 0.f;
 #pragma unroll
-        for (int r = 0; r < 8; ++r) s += red[r][c];
+        for (int r = 0; r < kRowLanes; ++r) s += red[r][c];
         if (a.bands == 1)
             db[n0 + c] = Ty::store(s);
         else
@@ -138,13 +142,13 @@ struct Bands {
 };
 
 Bands bands_of(int dtype, int M, int N) {
-    const int cols = dtype == kF32 ? 128 : 256;
+    const int cols = kColLanes * (dtype == kF32 ? 4 : 8);
     Bands b;
     b.blocks = (N + cols - 1) / cols;
-    // at most 128 bands, each of 8 rows at least; one where the column blocks
+    // at most 32 bands, whose sums the last workgroup of a column block adds up
+    // with two round trips to memory; one band where the column blocks
     // outnumber the arrival counters
-    b.band = (M + 127) / 128 < 64 ? 64 : ((M + 127) / 128 + 7) / 8 * 8;
-    while (b.band > 8 && (long long)b.blocks * ((M + b.band - 1) / b.band) < 512) b.band /= 2;
+    b.band = ((M + 31) / 32 + kRowLanes - 1) / kRowLanes * kRowLanes;
     if (b.blocks > kWorkspaceCounters) b.band = M;
     if (b.band < 1) b.band = 1;
     b.bands = M > 0 ? (M + b.band - 1) / b.band : 1;

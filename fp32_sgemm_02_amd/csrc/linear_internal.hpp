@@ -36,11 +36,8 @@ struct Prod {
     int act = SGEMM_ACT_NONE;
     int cvec = 0;   // 16-byte I/O of C, R, Z and bias (set by the launchers)
     int a_pad = 0;  // the rows of A are filled up with zeros to 16 bytes
-    // What the rounding of A left over, laid out as A (few-rows products only).
+    // What the rounding of A left over, laid out as A (few-rows kernels only).
     const void *lo = nullptr;
-    // K <= 64 and A (a_mc) given in two parts whose sum is meant: rows
-    // 0 .. K-1, and rows 64 .. 64+K-1, each summed against the same B.
-    int fold = 0;
 };
 
 // Tile kernels of 16-bit products (linear16.hip): bytes of partial sums (after
@@ -58,6 +55,8 @@ hipError_t launch_prod16_big(int dtype, const Prod &p, hipStream_t stream);
 constexpr int kFewRows = 64;
 size_t rows_workspace(int dtype, const Prod &p);
 hipError_t launch_rows(int dtype, const Prod &p, const Workspace &ws, hipStream_t stream);
+// K <= kFewRows, both operands with their own index contiguous.
+hipError_t launch_outer(int dtype, const Prod &p, hipStream_t stream);
 
 // G = dY * act'(Z) over M x N and its column sums (dtype SGEMM_DTYPE_*): G is
 // written where it is not null (rows of ldg values, 16-byte aligned, zeros from N

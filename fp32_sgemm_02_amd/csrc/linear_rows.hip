@@ -2,7 +2,8 @@
 // shapes of decoding and of small batches' gradients:
 //     rows_kernel   Y = act(X W^T + b) + R   W's rows run along k
 //     cols_kernel   dX = G W                 k runs over W's rows
-// Both are bound by reading W once: at M = 16 a weight value of two bytes is
+//     outer_kernel  dW = G^T X               k runs over the few rows
+// The first two are bound by reading W once: at M = 16 a weight value of two bytes is
 // used for 32 operations, far below the ~300 operations per byte at which the
 // matrix cores would be the limit.
 #include "stream_rows.hpp"
@@ -18,6 +19,25 @@ struct RowsGrid {
 };
 
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
+
+// The sum over slices of the partial sums at(s), in order, eight loads in flight
+// at a time (one after another each would wait for memory by itself).
+template <class F>
+__device__ __forceinline__ floatx4 sum_slices(int slices, F &&at) {
+    floatx4 sum = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < slices; s += 8) {
+        floatx4 v[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            v[q] = s + q < slices ? load_partial(at(s + q)) : floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (s + q < slices)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum[e] += v[q][e];
+    }
+    return sum;
+}
 
 // One strip of 16 rows of W per workgroup, the four waves taking contiguous
 // quarters of the slice's k and meeting in LDS.
@@ -64,20 +84,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(Prod p, RowsGrid gr) {
         };
         if (t < TB) store_partial(at(slice), sum);
         if (!arrive_last(gr.count + strip, gr.slices, &last)) return;
-        if (t < TB) {
-            sum = floatx4{0.f, 0.f, 0.f, 0.f};
-            for (int s = 0; s < gr.slices; s += 8) {
-                floatx4 v[8];
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    v[q] = s + q < gr.slices ? load_partial(at(s + q)) : floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    if (s + q < gr.slices)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) sum[e] += v[q][e];
-            }
-        }
+        if (t < TB) sum = sum_slices(gr.slices, at);
         if (tid == 0)
             __hip_atomic_store(gr.count + strip, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
@@ -151,38 +158,39 @@ __global__ void __launch_bounds__(512) rows_staged_kernel(Prod p, RowsGrid gr) {
     for (int b = wave; b < RB * TB; b += NW) store_partial(at(slice, b), sum_of(b));
     __syncthreads();   // red is read: its first word takes the flag
     if (!arrive_last(gr.count + strip, gr.slices, reinterpret_cast<int *>(smem))) return;
-    for (int b = wave; b < RB * TB; b += NW) {
-        floatx4 sum = {0.f, 0.f, 0.f, 0.f};
-        for (int s = 0; s < gr.slices; s += 8) {
-            floatx4 v[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-                v[q] = s + q < gr.slices ? load_partial(at(s + q, b)) : floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-                if (s + q < gr.slices)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sum[e] += v[q][e];
-        }
-        finish(b, sum);
-    }
+    for (int b = wave; b < RB * TB; b += NW)
+        finish(b, sum_slices(gr.slices, [&](int s) { return at(s, b); }));
     if (tid == 0)
         __hip_atomic_store(gr.count + strip, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 #endif
 }
 
+// A lane's V x V block of an operand whose own index is contiguous: it loads 16
+// bytes of each of V rows of k, which is V columns of V k values: fragments of V
+// products, once the block is turned (16-bit types: pairs of rows are
+// interleaved, 4 V byte permutes; fp32 needs none, a product step taking one
+// row).  Fragment c stands for column V i + c.
+template <int DT>
+__device__ __forceinline__ uintx4 turned(const uintx4 (&w)[Step<DT>::V], int c) {
+    uintx4 f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        if constexpr (DT == SGEMM_DTYPE_F32)
+            f[q] = w[q][c];
+        else   // halves c % 2 of dword c / 2 of rows 2q and 2q + 1
+            f[q] = __builtin_amdgcn_perm(w[2 * q + 1][c / 2], w[2 * q][c / 2],
+                                         (c & 1) ? 0x07060302u : 0x05040100u);
+    }
+    return f;
+}
+
 // dX = G W: a strip of 16 V columns of W per workgroup (V values to 16
-// bytes), k walking W's rows.  A lane loads 16 bytes of each of V rows, which
-// is V columns of V k values: the fragments of V products, once the V x V
-// block is turned (16-bit types: pairs of rows are interleaved, 4 V byte
-// permutes per step; fp32 needs none, a product step taking one row).
-// Product c of the block stands for column V i + c of the strip.  LO: G in two
-// parts.
-template <int DT, int TB, bool LO>
-__global__ void __launch_bounds__(kThreads) cols_kernel(Prod p, RowsGrid gr) {
+// bytes), k walking W's rows, turned in registers.  LO: G in two parts.
+template <int DT, int TB, bool LO, int NW>
+__global__ void __launch_bounds__(64 * NW) cols_kernel(Prod p, RowsGrid gr) {
     using T = typename Type<DT>::T;
     constexpr int V = Step<DT>::V, KS = Step<DT>::K, COLS = 16 * V;
-    __shared__ floatx4 red[2][V][TB][64];
+    __shared__ floatx4 red[NW / 2][V * TB][64];
     __shared__ int last;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -195,8 +203,23 @@ __global__ void __launch_bounds__(kThreads) cols_kernel(Prod p, RowsGrid gr) {
     struct Round {
         uintx4 w[V], x[TB], l[LO ? TB : 1];
     } a, b;
+    // 16-byte loads throughout unless the strip ends inside a lane's columns;
+    // lanes past the end read the strip's first columns (not stored)
+    const bool even = n0 + COLS <= p.N || (p.N % V == 0 && p.N - n0 >= V);
+    const T *Bf = static_cast<const T *>(p.B) + (cols >= V ? col : n0);
     auto load = [&](Round &r, int k) {
         const int kg = k + V * g;
+        if (even && k + KS <= ke) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) r.w[e] = load_whole<DT>(Bf + (long long)(kg + e) * p.ldb);
+#pragma unroll
+            for (int t = 0; t < TB; ++t) {
+                const long long at = (long long)min(16 * t + i, p.M - 1) * p.lda + kg;
+                r.x[t] = load_whole<DT>(static_cast<const T *>(p.A) + at);
+                if constexpr (LO) r.l[t] = load_whole<DT>(static_cast<const T *>(p.lo) + at);
+            }
+            return;
+        }
 #pragma unroll
         for (int e = 0; e < V; ++e)
             r.w[e] = load_frag<DT>(B + (long long)(kg + e) * p.ldb, kg + e < ke ? cols : 0);
@@ -215,15 +238,7 @@ __global__ void __launch_bounds__(kThreads) cols_kernel(Prod p, RowsGrid gr) {
     auto products = [&](const Round &r) {
 #pragma unroll
         for (int c = 0; c < V; ++c) {
-            uintx4 f;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if constexpr (DT == SGEMM_DTYPE_F32)
-                    f[q] = r.w[q][c];
-                else   // halves c % 2 of dword c / 2 of rows 2q and 2q + 1
-                    f[q] = __builtin_amdgcn_perm(r.w[2 * q + 1][c / 2], r.w[2 * q][c / 2],
-                                                 (c & 1) ? 0x07060302u : 0x05040100u);
-            }
+            const uintx4 f = turned<DT>(r.w, c);
 #pragma unroll
             for (int t = 0; t < TB; ++t) {
                 acc[c][t] = mfma_step<DT>(f, r.x[t], acc[c][t]);
@@ -232,7 +247,7 @@ __global__ void __launch_bounds__(kThreads) cols_kernel(Prod p, RowsGrid gr) {
         }
     };
     // the waves take the steps of the slice in turn
-    constexpr int ST = kWaves * KS;
+    constexpr int ST = NW * KS;
     const int k0 = ks + wave * KS;
     if (k0 < ke) {
         load(a, k0);
@@ -248,57 +263,135 @@ __global__ void __launch_bounds__(kThreads) cols_kernel(Prod p, RowsGrid gr) {
             pipeline_fence();
         }
     }
-    // waves 2 and 3 hand their sums to 0 and 1, then 1 to 0: a fixed order
+    // the upper half of the waves hand their sums to the lower, down to the
+    // first wave, which leaves the workgroup's in red[0]
 #pragma unroll
-    for (int half = 2; half >= 1; half /= 2) {
+    for (int half = NW / 2; half >= 1; half /= 2) {
         __syncthreads();
         if (wave >= half && wave < 2 * half)
 #pragma unroll
-            for (int c = 0; c < V; ++c)
-#pragma unroll
-                for (int t = 0; t < TB; ++t) red[wave - half][c][t][lane] = acc[c][t];
+            for (int j = 0; j < V * TB; ++j) red[wave - half][j][lane] = acc[j / TB][j % TB];
         __syncthreads();
         if (wave < half)
 #pragma unroll
-            for (int c = 0; c < V; ++c)
+            for (int j = 0; j < V * TB; ++j) {
+                const floatx4 v = red[wave][j][lane];
 #pragma unroll
-                for (int t = 0; t < TB; ++t)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[c][t][e] += red[wave][c][t][lane][e];
+                for (int e = 0; e < 4; ++e) acc[j / TB][j % TB][e] += v[e];
+            }
     }
+    if (wave == 0)
+#pragma unroll
+        for (int j = 0; j < V * TB; ++j) red[0][j][lane] = acc[j / TB][j % TB];
+    __syncthreads();
     if (gr.slices > 1) {
+        // every wave takes a share of the accumulators, eight slices' loads in
+        // flight at a time
         auto at = [&](int s, int j) {
             return gr.part + ((((long long)s * gr.strips + strip) * (V * TB) + j) * 64 + lane) * 4;
         };
-        if (wave == 0)
-#pragma unroll
-            for (int j = 0; j < V * TB; ++j) store_partial(at(slice, j), acc[j / TB][j % TB]);
+        for (int j = wave; j < V * TB; j += NW) store_partial(at(slice, j), red[0][j][lane]);
         if (!arrive_last(gr.count + strip, gr.slices, &last)) return;
-        if (wave == 0) {
-#pragma unroll
-            for (int j = 0; j < V * TB; ++j) acc[j / TB][j % TB] = load_partial(at(0, j));
-            for (int s = 1; s < gr.slices; ++s)
-#pragma unroll
-                for (int j = 0; j < V * TB; ++j) {
-                    const floatx4 v = load_partial(at(s, j));
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[j / TB][j % TB][e] += v[e];
-                }
-        }
+        for (int j = wave; j < V * TB; j += NW) red[0][j][lane] = sum_slices(gr.slices, [&](int s) { return at(s, j); });
         if (tid == 0)
             __hip_atomic_store(gr.count + strip, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
     }
-    if (wave != 0) return;
+    // result element r of row block t: V adjacent columns of row 16 t + i
+    for (int u = wave; u < 4 * TB; u += NW) {
+        const int t = u >> 2, r = u & 3, m = 16 * t + i;
+        float v[V];
 #pragma unroll
-    for (int t = 0; t < TB; ++t) {
-        const int m = 16 * t + i;
-        if (m >= p.M) continue;
+        for (int c = 0; c < V; ++c)
+            v[c] = reinterpret_cast<const float *>(&red[0][c * TB + t][lane])[r];
+        if (m < p.M) finish_run<DT, SGEMM_ACT_NONE>(p, m, n0 + V * (4 * g + r), v);
+    }
+}
+
+// dW = G^T X with at most 64 rows of G and X (LO: G in two parts): bound by
+// writing dW.  A wave computes 16 V x 16 V of it from S steps of k, and each lane
+// stores 16 bytes of a row at a time: no ring and no barriers.  X is turned in
+// registers; G waits in LDS, from where a lane takes one column of its block at
+// a time (so the walk over the columns is a loop).  Product (c, c') of the wave is rows V i + c of dW (lane i)
+// and columns V (4g + r) + c' (result element r).
+template <int DT, int S, bool LO>
+__global__ void __launch_bounds__(kThreads) outer_kernel(Prod p, int blocks_n) {
+    using T = typename Type<DT>::T;
+    constexpr int V = Step<DT>::V, KS = Step<DT>::K, B = 16 * V, PARTS = LO ? 2 : 1;
+    __shared__ uintx4 held[kWaves][PARTS][S][V][64];
+    const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int block = blockIdx.x * kWaves + wave;
+    const int m0 = block / blocks_n * B, n0 = block % blocks_n * B;
+    if (m0 >= p.M) return;
+    const int am = m0 + V * i, bn = n0 + V * i;
+    // 16-byte loads throughout unless the block ends inside a lane's values;
+    // lanes past an end read the block's first values (not stored), rows past K
+    // the last one (zeroed)
+    auto even = [&](int at0, int n) { return at0 + B <= n || (n % V == 0 && n - at0 >= V); };
+    const bool fast = p.K > 0 && even(m0, p.M) && even(n0, p.N);   // K == 0: no row to read
+    const int amf = am + V <= p.M ? am : m0, bnf = bn + V <= p.N ? bn : n0;
+    uintx4 fb[S][V];
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        uintx4 a[PARTS][V], b[V];
+        if (fast) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const int k = s * KS + V * g + e;
+                const bool in = k < p.K;
+                const long long kc = in ? k : p.K - 1;
+                b[e] = load_whole<DT>(static_cast<const T *>(p.B) + kc * p.ldb + bnf, in);
+                a[0][e] = load_whole<DT>(static_cast<const T *>(p.A) + kc * p.lda + amf, in);
+                if constexpr (LO)
+                    a[1][e] = load_whole<DT>(static_cast<const T *>(p.lo) + kc * p.lda + amf, in);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const int k = s * KS + V * g + e;
+                const bool in = k < p.K;
+                const long long at = (long long)k * p.lda + am;
+                b[e] = load_frag<DT>(static_cast<const T *>(p.B) + (long long)k * p.ldb + bn,
+                                     in ? p.N - bn : 0);
+                a[0][e] = load_frag<DT>(static_cast<const T *>(p.A) + at, in ? p.M - am : 0);
+                if constexpr (LO)
+                    a[1][e] = load_frag<DT>(static_cast<const T *>(p.lo) + at, in ? p.M - am : 0);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q) held[wave][q][s][e][lane] = a[q][e];
+#pragma unroll
+        for (int c = 0; c < V; ++c) fb[s][c] = turned<DT>(b, c);
+    }
+    const int rows = min(V, p.M - am);   // rows of this lane inside dW
+#pragma unroll 1
+    for (int c = 0; c < V; ++c) {
+        floatx4 acc[V];
+#pragma unroll
+        for (int d = 0; d < V; ++d) acc[d] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q) {
+                T col[V];   // column c of this lane's block (a lane reads its own values)
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    col[e] = reinterpret_cast<const T *>(&held[wave][q][s][e][lane])[c];
+                uintx4 fa;
+                __builtin_memcpy(&fa, col, 16);
+#pragma unroll
+                for (int d = 0; d < V; ++d) acc[d] = mfma_step<DT>(fb[s][d], fa, acc[d]);
+            }
+        if (c >= rows) continue;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             float v[V];
 #pragma unroll
-            for (int c = 0; c < V; ++c) v[c] = acc[c][t][r];
-            finish_run<DT, SGEMM_ACT_NONE>(p, m, n0 + V * (4 * g + r), v);
+            for (int d = 0; d < V; ++d) v[d] = acc[d][r];
+            finish_run<DT, SGEMM_ACT_NONE>(p, am + c, n0 + V * (4 * g + r), v);
         }
     }
 }
@@ -340,7 +433,7 @@ PlanRows plan_rows(int dtype, const Prod &p) {
         // four steps at least
         if (q.strips < kCUs && q.strips <= kWorkspaceCounters) {
             s = (2 * kCUs + q.strips - 1) / q.strips;
-            const int most = p.K / (kWaves * 4 * step);
+            const int most = p.K / (kWaves * 4 * step);   // (or two for each of eight waves)
             if (s > most) s = most;
             if (s > 64) s = 64;
         }
@@ -355,6 +448,7 @@ PlanRows plan_rows(int dtype, const Prod &p) {
 
 template <int DT, int TB>
 hipError_t launch_tb(const Prod &p, const PlanRows &q, const RowsGrid &gr, hipStream_t stream) {
+    constexpr int CW = TB == 1 ? 8 : 4;   // the sums of eight waves fit LDS for one block of rows
     const dim3 grid((unsigned)gr.strips * gr.slices), block(kThreads);
     if (q.staged && q.rb == 1)
         hipLaunchKernelGGL((rows_staged_kernel<DT, 1, TB>), grid, dim3(512), 0, stream, p, gr);
@@ -365,10 +459,10 @@ hipError_t launch_tb(const Prod &p, const PlanRows &q, const RowsGrid &gr, hipSt
     else if (!p.b_mc)
         hipLaunchKernelGGL((rows_kernel<DT, TB, TB == 1 ? 8 : 4>), grid, block, 0, stream, p, gr);
     else if (DT != SGEMM_DTYPE_F32 && p.lo)
-        hipLaunchKernelGGL((cols_kernel<DT, TB, DT != SGEMM_DTYPE_F32>), grid, block, 0, stream, p,
-                           gr);
+        hipLaunchKernelGGL((cols_kernel<DT, TB, DT != SGEMM_DTYPE_F32, CW>), grid, dim3(64 * CW), 0,
+                           stream, p, gr);
     else
-        hipLaunchKernelGGL((cols_kernel<DT, TB, false>), grid, block, 0, stream, p, gr);
+        hipLaunchKernelGGL((cols_kernel<DT, TB, false, CW>), grid, dim3(64 * CW), 0, stream, p, gr);
     return hipGetLastError();
 }
 
@@ -385,7 +479,38 @@ hipError_t launch_dt(Prod p, const Workspace &ws, hipStream_t stream) {
     }
 }
 
+template <int DT, int S>
+hipError_t launch_steps(const Prod &p, hipStream_t stream) {
+    constexpr int B = 16 * Step<DT>::V;
+    const int bn = (p.N + B - 1) / B;
+    const long long blocks = (long long)((p.M + B - 1) / B) * bn;
+    const dim3 grid((unsigned)((blocks + kWaves - 1) / kWaves));
+    if (DT != SGEMM_DTYPE_F32 && p.lo)
+        hipLaunchKernelGGL((outer_kernel<DT, S, DT != SGEMM_DTYPE_F32>), grid, dim3(kThreads), 0,
+                           stream, p, bn);
+    else
+        hipLaunchKernelGGL((outer_kernel<DT, S, false>), grid, dim3(kThreads), 0, stream, p, bn);
+    return hipGetLastError();
+}
+
+template <int DT>
+hipError_t launch_outer_dt(Prod p, hipStream_t stream) {
+    constexpr int KS = Step<DT>::K;
+    p.cvec = epilogue_vec(p, (int)sizeof(typename Type<DT>::T));
+    if (p.K <= KS) return launch_steps<DT, 1>(p, stream);
+    if (DT != SGEMM_DTYPE_F32 || p.K <= 2 * KS) return launch_steps<DT, 2>(p, stream);
+    return launch_steps<DT, DT == SGEMM_DTYPE_F32 ? 4 : 2>(p, stream);
+}
+
 }  // namespace
+
+hipError_t launch_outer(int dtype, const Prod &p, hipStream_t stream) {
+    switch (dtype) {
+    case SGEMM_DTYPE_BF16: return launch_outer_dt<SGEMM_DTYPE_BF16>(p, stream);
+    case SGEMM_DTYPE_F16: return launch_outer_dt<SGEMM_DTYPE_F16>(p, stream);
+    default: return launch_outer_dt<SGEMM_DTYPE_F32>(p, stream);
+    }
+}
 
 size_t rows_workspace(int dtype, const Prod &p) {
     const PlanRows q = plan_rows(dtype, p);

@@ -66,14 +66,24 @@ __global__ void __launch_bounds__(kThreads) router_kernel(Moe m, MoeWs s) {
         }
         // U chunks' loads in flight: a few tokens' logits wait for memory only
         constexpr int U = EPW == 1 ? 4 : 2;
-        for (int d0 = lane * V; d0 < m.D; d0 += U * 64 * V) {
+        for (int d1 = 0; d1 < m.D; d1 += U * 64 * V) {
+            const int d0 = d1 + lane * V;
             uintx4 a[U], b[U][EPW];
+            if (d1 + U * 64 * V <= m.D) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int d = d0 + u * 64 * V;
-                a[u] = load_frag<DT>(x + d, m.D - d);
+                for (int u = 0; u < U; ++u) {
+                    a[u] = load_whole<DT>(x + d0 + u * 64 * V);
 #pragma unroll
-                for (int q = 0; q < EPW; ++q) b[u][q] = load_frag<DT>(w[q] + d, m.D - d);
+                    for (int q = 0; q < EPW; ++q) b[u][q] = load_whole<DT>(w[q] + d0 + u * 64 * V);
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int d = d0 + u * 64 * V;
+                    a[u] = load_frag<DT>(x + d, m.D - d);
+#pragma unroll
+                    for (int q = 0; q < EPW; ++q) b[u][q] = load_frag<DT>(w[q] + d, m.D - d);
+                }
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {

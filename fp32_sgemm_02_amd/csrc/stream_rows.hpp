@@ -52,6 +52,17 @@ __device__ __forceinline__ uintx4 load_frag(const typename Type<DT>::T *p, int n
     return v;
 }
 
+// V values from p on, all inside; zeros where !keep (p is then any readable
+// place).  Branch-free: loads behind per-lane branches wait for one another.
+template <int DT>
+__device__ __forceinline__ uintx4 load_whole(const typename Type<DT>::T *p, bool keep = true) {
+    uintx4 v;
+    __builtin_memcpy(&v, p, 16);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = keep ? v[q] : 0u;
+    return v;
+}
+
 // acc[r][t] += the products over k in [k0, k1) of RB weight rows (w[r]: this
 // lane's row of 16-row block r) and TB token rows (x[t]), k0 a multiple of the
 // step; both pointers at k = 0, kend the length of the rows.  Two register
