@@ -556,6 +556,50 @@ int run(Problem p, hipStream_t stream, const sgemm_config *cfg, bool noalloc = f
     return st;
 }
 
+// Workspace bytes (after the counters) of p's automatic plan, the largest of its
+// parts' (see run).
+size_t plan_workspace(const Problem &p) {
+    if (p.M == 0 || p.N == 0 || p.K == 0) return 0;
+    Choice ch;
+    Strips sp;
+    if (resolve(p, nullptr, ch, &sp) != 0) return 0;
+    const int m1 = p.M - sp.rows, n1 = p.N - sp.cols;
+    size_t most = choice_workspace(main_part(p, sp), ch);
+    auto part = [&](const Problem &q) {
+        Choice c;
+        if (resolve(q, nullptr, c) == 0 && choice_workspace(q, c) > most) most = choice_workspace(q, c);
+    };
+    if (sp.cols) {
+        Problem q = p;
+        q.M = m1;
+        q.N = sp.cols;
+        q.B = p.trans_b ? p.B + (long long)n1 * p.ldb : p.B + n1;
+        q.C = p.C + n1;
+        if (p.bias) q.bias = p.bias + n1;
+        part(q);
+    }
+    if (sp.rows) {
+        Problem q = p;
+        q.M = sp.rows;
+        q.A = p.A + (long long)m1 * p.lda;
+        q.C = p.C + (long long)m1 * p.ldc;
+        part(q);
+    }
+    return most;
+}
+
+int fused_linear(const Problem &p, hipStream_t stream) {
+    Choice ch;
+    const int st = resolve(p, nullptr, ch);
+    if (st != 0) return st;
+    if (ch.variant != SGEMM_VARIANT_MFMA || ch.streamk || !ch.vec) return kNotFused;
+    int count = 0;
+    const TileEntry &t = family(ch.variant, &count)[ch.tile];
+    if (!(t.desc.flags & SGEMM_TILE_DIRECT) || !t.fused) return kNotFused;
+    const hipError_t e = t.fused(p, ch.group_m, stream);
+    return e == hipErrorNotSupported ? kNotFused : to_status(e);
+}
+
 // ---- 16-bit inputs -----------------------------------------------------------
 // The 16-bit tile of least estimated time for the word problem pw (the fp32
 // cost model over the 16-bit tile list), or -1.
@@ -657,6 +701,11 @@ Problem make_problem(int trans_a, int trans_b, int M, int N, int K, float alpha,
 }
 
 }  // namespace
+
+int run_fused_linear(const Problem &p, hipStream_t stream) { return fused_linear(p, stream); }
+int run_product(const Problem &p, hipStream_t stream) { return run(p, stream, nullptr); }
+size_t product_workspace(const Problem &p) { return plan_workspace(p); }
+
 }  // namespace sg
 
 extern "C" {

@@ -643,8 +643,22 @@ mfma_direct_kernel(Problem p, int tiles_m, int tiles_n, int group_m, int cvec, S
 #pragma unroll
                             for (int c = 0; c < 4; ++c) v[c] = fmaf(p.beta, old[c], v[c]);
                         }
+                        if constexpr (ACT < 0) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) v[c] = finish(v[c], cg * 4 + c);
+                            for (int c = 0; c < 4; ++c) v[c] = finish(v[c], cg * 4 + c);
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) v[c] += bcol[cg * 4 + c];
+                            if (p.Z) __builtin_memcpy(p.Z + (long long)gm * p.ldz + gn, &v, 16);
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) v[c] = activate_t<ACT>(v[c]);
+                            if (p.R) {
+                                floatx4 res;
+                                __builtin_memcpy(&res, p.R + (long long)gm * p.ldr + gn, 16);
+#pragma unroll
+                                for (int c = 0; c < 4; ++c) v[c] += res[c];
+                            }
+                        }
                         __builtin_nontemporal_store(v, dst);
                     } else {
 #pragma unroll
@@ -652,7 +666,10 @@ mfma_direct_kernel(Problem p, int tiles_m, int tiles_n, int group_m, int cvec, S
                             if (gn + c >= p.N) continue;
                             float out = v[c];
                             if (read_c) out = fmaf(p.beta, crow[gn + c], out);
-                            crow[gn + c] = finish(out, cg * 4 + c);
+                            if (EPI && p.Z) p.Z[(long long)gm * p.ldz + gn + c] = out + bcol[cg * 4 + c];
+                            out = finish(out, cg * 4 + c);
+                            if (EPI && p.R) out += p.R[(long long)gm * p.ldr + gn + c];
+                            crow[gn + c] = out;
                         }
                     }
                 }

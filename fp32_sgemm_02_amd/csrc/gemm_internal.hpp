@@ -37,6 +37,12 @@ struct Problem {
     // scratch_bytes for the sums.  Null: the workspace of workspace_acquire.
     void *scratch = nullptr;
     size_t scratch_bytes = 0;
+    // A linear layer's further epilogue, applied by the direct-load tiles' fused
+    // launchers only: Z receives the sum plus bias, R is added after the activation.
+    const float *R = nullptr;
+    long long ldr = 0;
+    float *Z = nullptr;
+    long long ldz = 0;
     __host__ __device__ bool has_epilogue() const {
         return bias != nullptr || act != SGEMM_ACT_NONE;
     }
@@ -114,6 +120,8 @@ struct Workspace {
 };
 // kind: buffers of different kinds are cached apart (0: the products' partial
 // sums; 1: the feed-forward operators, several launches of which share one).
+// Under capture those of kind 1 are ordinary allocations, one for all calls that
+// one capture records on one stream, kept with the cached ones.
 hipError_t workspace_acquire(size_t bytes, hipStream_t stream, const Problem &p, Workspace &w,
                              int kind = 0);
 hipError_t workspace_release(const Workspace &w, hipStream_t stream);
@@ -169,6 +177,18 @@ int small_choice(const Problem &p);
 // no epilogue, C = beta * C.  The alpha == 0 / K == 0 case, and the bias and
 // activation pass after a kernel that does not apply them itself (beta = 1).
 hipError_t launch_elementwise(const Problem &p, float beta, hipStream_t stream);
+
+// The fp32 product of a linear layer (R, Z, bias and act of p) through the fused
+// launcher of the tile that automatic dispatch gives it.  Returns a status, or
+// kNotFused, before any launch, where that tile has none for these operands
+// (or the product is better split over k).
+constexpr int kNotFused = -1000;
+int run_fused_linear(const Problem &p, hipStream_t stream);
+// Any fp32 product as the entry points run it (checks included), and the bytes of
+// partial sums that its automatic plan takes, for callers that bring them in
+// Problem::scratch.
+int run_product(const Problem &p, hipStream_t stream);
+size_t product_workspace(const Problem &p);
 
 // ---- device helpers shared by the families ---------------------------------
 

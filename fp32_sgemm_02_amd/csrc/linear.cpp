@@ -46,14 +46,16 @@ int with_workspace(size_t bytes, bool counters, hipStream_t stream, F &&f) {
     return st != 0 ? st : to_status(e);
 }
 
-// Part of a workspace: the same counters, the sums from `offset` bytes on.
-Workspace part_of(const Workspace &ws, size_t offset) {
-    Workspace w = ws;
-    w.ptr = static_cast<unsigned char *>(ws.ptr) + offset;
-    return w;
+// An fp32 product with its partial sums at the front of the workspace.
+int run_in(Problem p, const Workspace &ws, size_t bytes, hipStream_t stream) {
+    if (bytes) {
+        p.scratch = ws.base;
+        p.scratch_bytes = bytes;
+    }
+    return run_product(p, stream);
 }
 
-size_t product_workspace(int dtype, const Prod &p, bool rows) {
+size_t ours_workspace(int dtype, const Prod &p, bool rows) {
     return rows ? rows_workspace(dtype, p) : prod16_workspace(dtype, p);
 }
 hipError_t launch_product(int dtype, const Prod &p, bool rows, const Workspace &ws,
@@ -64,34 +66,49 @@ hipError_t launch_product(int dtype, const Prod &p, bool rows, const Workspace &
 int run_linear(int dtype, const Prod &p, hipStream_t stream) {
     const bool rows = p.M <= kFewRows;
     if (dtype != SGEMM_DTYPE_F32 || rows) {
-        const size_t bytes = product_workspace(dtype, p, rows);
+        const size_t bytes = ours_workspace(dtype, p, rows);
         return with_workspace(bytes, false, stream, [&](const Workspace &ws) {
             return to_status(launch_product(dtype, p, rows, ws, stream));
         });
     }
-    // fp32: the library's product with the bias in its epilogue, then one
-    // elementwise pass for what comes after the sum
+    // fp32: the library's product with its fused epilogue where the tile has one
+    // that serves these operands; otherwise with the bias in the product's
+    // epilogue and one elementwise pass for what comes after
     const float *A = static_cast<const float *>(p.A), *B = static_cast<const float *>(p.B);
     const float *bias = static_cast<const float *>(p.bias), *R = static_cast<const float *>(p.R);
     float *Y = static_cast<float *>(p.C), *Z = static_cast<float *>(p.Z);
-    auto product = [&](float *C, int ldc, int act) {
-        return sgemm_epilogue(0, 1, p.M, p.N, p.K, 1.f, A, (int)p.lda, B, (int)p.ldb, 0.f, C, ldc,
-                              bias, act, stream);
-    };
-    if (!R && !Z) return product(Y, (int)p.ldc, p.act);
-    if (Z) {
-        const int st = product(Z, (int)p.ldz, SGEMM_ACT_NONE);
-        return st != 0 ? st
-                       : to_status(launch_finish32(p.M, p.N, Z, p.ldz, p.act, R, p.ldr, Y, p.ldc,
-                                                   stream));
+    Problem q{p.M, p.N, p.K, 1.f, 0.f, A, p.lda, B, p.ldb, Y, p.ldc};
+    q.trans_b = 1;
+    q.bias = bias;
+    q.act = p.act;
+    if ((R || Z) && p.K > 0) {
+        Problem f = q;
+        f.R = R;
+        f.ldr = p.ldr;
+        f.Z = Z;
+        f.ldz = p.ldz;
+        const int st = run_fused_linear(f, stream);
+        if (st != kNotFused) return st;
     }
-    const size_t ld = round_up(p.N, 4);
-    return with_workspace(ld * p.M * 4, false, stream, [&](const Workspace &ws) {
-        float *t = static_cast<float *>(ws.ptr);
-        const int st = product(t, (int)ld, p.act);
-        return st != 0 ? st
-                       : to_status(launch_finish32(p.M, p.N, t, ld, SGEMM_ACT_NONE, R, p.ldr, Y,
-                                                   p.ldc, stream));
+    // R may be Y, so the sum goes elsewhere first: to Z, or to the workspace
+    const bool temp = R && !Z;
+    const long long ld = (long long)round_up(p.N, 4);
+    if (Z) {
+        q.C = Z;
+        q.ldc = p.ldz;
+        q.act = SGEMM_ACT_NONE;
+    } else if (temp) {
+        q.C = reinterpret_cast<float *>(uintptr_t{4096});   // (for the plan: an aligned place)
+        q.ldc = ld;
+    }
+    const size_t sums = round_up(product_workspace(q), 256);
+    return with_workspace(sums + (temp ? (size_t)ld * p.M * 4 : 0), false, stream,
+                          [&](const Workspace &ws) -> int {
+        if (temp) q.C = reinterpret_cast<float *>(static_cast<unsigned char *>(ws.ptr) + sums);
+        const int st = run_in(q, ws, sums, stream);
+        if (st != 0 || (!R && !Z)) return st;
+        return to_status(launch_finish32(p.M, p.N, q.C, q.ldc, temp ? SGEMM_ACT_NONE : p.act, R,
+                                         p.ldr, Y, p.ldc, stream));
     });
 }
 
@@ -138,46 +155,56 @@ int run_backward(int dtype, const Backward &b, hipStream_t stream) {
     dw.a_mc = dw.b_mc = 1;
     dx.a_pad = dw.a_pad = make_g;
     const bool dx_ours = want_dx && (!f32 || few), dw_ours = want_dw && (!f32 || few);
+    auto op32 = [&](int ta, int M, int N, int K, const void *A, long long lda, const void *B, int ldb,
+                    void *C, int ldc) {
+        Problem q{M, N, K, 1.f, 0.f, static_cast<const float *>(A), lda, static_cast<const float *>(B),
+                  ldb, static_cast<float *>(C), ldc};
+        q.trans_a = ta;
+        return q;
+    };
+    // fp32 products of more than a few rows run as the library's own (the address
+    // of G, when it is made, is as well aligned as any)
+    const void *g_at = make_g ? reinterpret_cast<const void *>(uintptr_t{4096}) : b.dY;
+    Problem dx32 = op32(0, b.M, b.K, b.N, g_at, ldg, b.W, b.ldw, b.dX, b.lddx);
+    Problem dw32 = op32(1, b.N, b.K, b.M, g_at, ldg, b.X, b.ldx, b.dW, b.lddw);
+    const bool dx_lib = want_dx && !dx_ours, dw_lib = want_dw && !dw_ours;
     size_t scratch = want_db ? grad_workspace(dtype, b.M, b.N) : 0;
+    if (dx_lib && product_workspace(dx32) > scratch) scratch = product_workspace(dx32);
+    if (dw_lib && product_workspace(dw32) > scratch) scratch = product_workspace(dw32);
     if (dx_ours) {
-        const size_t s = product_workspace(dtype, dx, few);
+        const size_t s = ours_workspace(dtype, dx, few);
         if (s > scratch) scratch = s;
     }
     if (dw_ours && !few) {
-        const size_t s = product_workspace(dtype, dw, false);
+        const size_t s = ours_workspace(dtype, dw, false);
         if (s > scratch) scratch = s;
     }
-    return with_workspace(g_bytes + scratch, false, stream, [&](const Workspace &ws) -> int {
-        const Workspace rest = ws.ptr ? part_of(ws, g_bytes) : ws;
+    // the workspace: the launches' partial sums, one after another's, then G
+    scratch = round_up(scratch, 256);
+    return with_workspace(scratch + g_bytes, false, stream, [&](const Workspace &ws) -> int {
         if (make_g || want_db) {
-            unsigned char *G = make_g ? static_cast<unsigned char *>(ws.ptr) : nullptr;
+            unsigned char *G = make_g ? static_cast<unsigned char *>(ws.ptr) + scratch : nullptr;
             void *lo = two ? G + (size_t)b.M * ldg * elem : nullptr;
             const hipError_t e =
                 launch_grad(dtype, b.M, b.N, b.dY, b.lddy, b.Z, b.ldz, b.act, G, lo, ldg,
-                            want_db ? b.db : nullptr, static_cast<float *>(rest.ptr),
-                            rest.counters, stream);
+                            want_db ? b.db : nullptr, static_cast<float *>(ws.ptr), ws.counters,
+                            stream);
             if (e != hipSuccess) return to_status(e);
-            if (make_g) dx.A = dw.A = G;
+            if (make_g) {
+                dx.A = dw.A = G;
+                dx32.A = dw32.A = reinterpret_cast<const float *>(G);
+            }
             dx.lo = dw.lo = lo;
         }
         if (want_dx) {
-            int st;
-            if (dx_ours)
-                st = to_status(launch_product(dtype, dx, few, rest, stream));
-            else
-                st = sgemm_op(0, 0, b.M, b.K, b.N, 1.f, static_cast<const float *>(dx.A), (int)ldg,
-                              static_cast<const float *>(b.W), b.ldw, 0.f,
-                              static_cast<float *>(b.dX), b.lddx, stream);
+            const int st = dx_lib ? run_in(dx32, ws, scratch, stream)
+                                  : to_status(launch_product(dtype, dx, few, ws, stream));
             if (st != 0) return st;
         }
-        if (want_dw) {
-            if (few) return to_status(launch_outer(dtype, dw, stream));
-            if (dw_ours) return to_status(launch_product(dtype, dw, false, rest, stream));
-            return sgemm_op(1, 0, b.N, b.K, b.M, 1.f, static_cast<const float *>(dw.A), (int)ldg,
-                            static_cast<const float *>(b.X), b.ldx, 0.f,
-                            static_cast<float *>(b.dW), b.lddw, stream);
-        }
-        return 0;
+        if (!want_dw) return 0;
+        if (dw_lib) return run_in(dw32, ws, scratch, stream);
+        return to_status(few ? launch_outer(dtype, dw, stream)
+                             : launch_product(dtype, dw, false, ws, stream));
     });
 }
 

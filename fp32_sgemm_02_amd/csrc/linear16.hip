@@ -392,7 +392,6 @@ hipError_t launch_layout(const Prod &p, const Grid16 &gr, bool ad, bool bd, hipS
 template <int DT>
 hipError_t launch_dt(Prod p, const Workspace &ws, hipStream_t stream) {
     const Plan16 q = plan16(p);
-    p.cvec = epilogue_vec(p, 2);
     if (q.big) return launch_prod16_big(DT, p, stream);
     Grid16 gr{};
     gr.tiles_m = (p.M + q.bm - 1) / q.bm;

@@ -34,7 +34,6 @@ struct Prod {
     void *Z = nullptr;
     long long ldz = 0;
     int act = SGEMM_ACT_NONE;
-    int cvec = 0;   // 16-byte I/O of C, R, Z and bias (set by the launchers)
     int a_pad = 0;  // the rows of A are filled up with zeros to 16 bytes
     // What the rounding of A left over, laid out as A (few-rows kernels only).
     const void *lo = nullptr;
@@ -99,10 +98,6 @@ hipError_t launch_finish32(int M, int N, const float *Z, long long ldz, int act,
 // Whether rows of an array take 16-byte accesses.
 __host__ __device__ inline bool rows16(const void *q, long long ld, int elem) {
     return reinterpret_cast<unsigned long long>(q) % 16 == 0 && ld * elem % 16 == 0;
-}
-inline int epilogue_vec(const Prod &p, int elem) {
-    return rows16(p.C, p.ldc, elem) && (!p.R || rows16(p.R, p.ldr, elem)) &&
-           (!p.Z || rows16(p.Z, p.ldz, elem)) && (!p.bias || rows16(p.bias, 16, elem));
 }
 
 // ---- device helpers ---------------------------------------------------------
@@ -298,7 +293,8 @@ __device__ __forceinline__ void with_act(int act, F &&f) {
 }
 
 // Bias, activation, residual and the store of the CN adjacent columns from n
-// on (n a multiple of 4, of 8 where CN >= 8) of row m < p.M.  R may be C: each
+// on of row m < p.M, 16 bytes at a time whatever their alignment (the target
+// takes any address), those at the end value by value.  R may be C: each
 // cell is read before it is written, by the same lane.
 template <int DT, int ACT, int CN>
 __device__ __forceinline__ void finish_run(const Prod &p, int m, int n, const float (&v)[CN]) {
@@ -315,16 +311,16 @@ __device__ __forceinline__ void finish_run(const Prod &p, int m, int n, const fl
     for (int h = 0; h < CN; h += W) {
         const int n1 = n + h;
         if (n1 >= p.N) return;
-        if (p.cvec && n1 + W <= p.N) {
+        if (n1 + W <= p.N) {   // (whole accesses go to any address)
             T t[W];
             float x[W], res[W];
             if (r) {
-                __builtin_memcpy(t, __builtin_assume_aligned(r + n1, BYTES), BYTES);
+                __builtin_memcpy(t, r + n1, BYTES);
 #pragma unroll
                 for (int e = 0; e < W; ++e) res[e] = Ty::load(t[e]);
             }
             if (bias) {
-                __builtin_memcpy(t, __builtin_assume_aligned(bias + n1, BYTES), BYTES);
+                __builtin_memcpy(t, bias + n1, BYTES);
 #pragma unroll
                 for (int e = 0; e < W; ++e) x[e] = v[h + e] + Ty::load(t[e]);
             } else {
@@ -334,14 +330,14 @@ __device__ __forceinline__ void finish_run(const Prod &p, int m, int n, const fl
             if (z) {
 #pragma unroll
                 for (int e = 0; e < W; ++e) t[e] = Ty::store(x[e]);
-                __builtin_memcpy(__builtin_assume_aligned(z + n1, BYTES), t, BYTES);
+                __builtin_memcpy(z + n1, t, BYTES);
             }
 #pragma unroll
             for (int e = 0; e < W; ++e) {
                 const float y = activate_t<ACT>(x[e]);
                 t[e] = Ty::store(r ? y + res[e] : y);
             }
-            __builtin_memcpy(__builtin_assume_aligned(c + n1, BYTES), t, BYTES);
+            __builtin_memcpy(c + n1, t, BYTES);
         } else {
 #pragma unroll
             for (int e = 0; e < W; ++e) {

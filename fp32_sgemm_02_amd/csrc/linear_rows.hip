@@ -310,21 +310,27 @@ __global__ void __launch_bounds__(64 * NW) cols_kernel(Prod p, RowsGrid gr) {
 
 // dW = G^T X with at most 64 rows of G and X (LO: G in two parts): bound by
 // writing dW.  A wave computes 16 V x 16 V of it from S steps of k, and each lane
-// stores 16 bytes of a row at a time: no ring and no barriers.  X is turned in
+// stores 16 bytes of a row at a time: no ring and no barriers.  With few blocks
+// the four waves of a workgroup share one, each taking some of its columns of G
+// (SPLIT 4: 16 rows, 1024 x 1024 14 -> 9 us; with many, the repeated loads cost
+// more: 16 rows, 14336 x 4096 49 -> 57 us).  X is turned in
 // registers; G waits in LDS, from where a lane takes one column of its block at
 // a time (so the walk over the columns is a loop).  Product (c, c') of the wave is rows V i + c of dW (lane i)
-// and columns V (4g + r) + c' (result element r).
-template <int DT, int S, bool LO>
+// and columns V (4r + g) + c' (result element r).
+template <int DT, int S, bool LO, int SPLIT>
 __global__ void __launch_bounds__(kThreads) outer_kernel(Prod p, int blocks_n) {
     using T = typename Type<DT>::T;
     constexpr int V = Step<DT>::V, KS = Step<DT>::K, B = 16 * V, PARTS = LO ? 2 : 1;
     __shared__ uintx4 held[kWaves][PARTS][S][V][64];
     const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int block = blockIdx.x * kWaves + wave;
+    static_assert(V % SPLIT == 0 && (SPLIT == 1 || SPLIT == kWaves), "whole columns");
+    const int block = SPLIT == 1 ? blockIdx.x * kWaves + wave : blockIdx.x;
     const int m0 = block / blocks_n * B, n0 = block % blocks_n * B;
     if (m0 >= p.M) return;
-    const int am = m0 + V * i, bn = n0 + V * i;
+    // (X's lanes are dealt so that the four lanes that store one row side by
+    // side store 64 bytes in a row)
+    const int am = m0 + V * i, bn = n0 + V * (4 * (i & 3) + (i >> 2));
     // 16-byte loads throughout unless the block ends inside a lane's values;
     // lanes past an end read the block's first values (not stored), rows past K
     // the last one (zeroed)
@@ -368,7 +374,8 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(Prod p, int blocks_n) {
     }
     const int rows = min(V, p.M - am);   // rows of this lane inside dW
 #pragma unroll 1
-    for (int c = 0; c < V; ++c) {
+    for (int q = 0; q < V / SPLIT; ++q) {
+        const int c = SPLIT == 1 ? q : wave * (V / SPLIT) + q;
         floatx4 acc[V];
 #pragma unroll
         for (int d = 0; d < V; ++d) acc[d] = floatx4{0.f, 0.f, 0.f, 0.f};
@@ -391,7 +398,7 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(Prod p, int blocks_n) {
             float v[V];
 #pragma unroll
             for (int d = 0; d < V; ++d) v[d] = acc[d][r];
-            finish_run<DT, SGEMM_ACT_NONE>(p, am + c, n0 + V * (4 * g + r), v);
+            finish_run<DT, SGEMM_ACT_NONE>(p, am + c, n0 + V * (4 * r + g), v);
         }
     }
 }
@@ -469,7 +476,6 @@ hipError_t launch_tb(const Prod &p, const PlanRows &q, const RowsGrid &gr, hipSt
 template <int DT>
 hipError_t launch_dt(Prod p, const Workspace &ws, hipStream_t stream) {
     const PlanRows q = plan_rows(DT, p);
-    p.cvec = epilogue_vec(p, (int)sizeof(typename Type<DT>::T));
     const RowsGrid gr{q.strips, q.slices, q.kslice, q.width, static_cast<float *>(ws.ptr),
                       ws.counters};
     switch (q.tb) {
@@ -479,27 +485,32 @@ hipError_t launch_dt(Prod p, const Workspace &ws, hipStream_t stream) {
     }
 }
 
+template <int DT, int S, int SPLIT>
+hipError_t launch_steps(const Prod &p, long long blocks, int bn, hipStream_t stream) {
+    const dim3 grid((unsigned)(SPLIT == 1 ? (blocks + kWaves - 1) / kWaves : blocks));
+    if (DT != SGEMM_DTYPE_F32 && p.lo)
+        hipLaunchKernelGGL((outer_kernel<DT, S, DT != SGEMM_DTYPE_F32, SPLIT>), grid, dim3(kThreads),
+                           0, stream, p, bn);
+    else
+        hipLaunchKernelGGL((outer_kernel<DT, S, false, SPLIT>), grid, dim3(kThreads), 0, stream, p, bn);
+    return hipGetLastError();
+}
+
 template <int DT, int S>
-hipError_t launch_steps(const Prod &p, hipStream_t stream) {
+hipError_t launch_split(const Prod &p, hipStream_t stream) {
     constexpr int B = 16 * Step<DT>::V;
     const int bn = (p.N + B - 1) / B;
     const long long blocks = (long long)((p.M + B - 1) / B) * bn;
-    const dim3 grid((unsigned)((blocks + kWaves - 1) / kWaves));
-    if (DT != SGEMM_DTYPE_F32 && p.lo)
-        hipLaunchKernelGGL((outer_kernel<DT, S, DT != SGEMM_DTYPE_F32>), grid, dim3(kThreads), 0,
-                           stream, p, bn);
-    else
-        hipLaunchKernelGGL((outer_kernel<DT, S, false>), grid, dim3(kThreads), 0, stream, p, bn);
-    return hipGetLastError();
+    return blocks <= 2 * kCUs ? launch_steps<DT, S, kWaves>(p, blocks, bn, stream)
+                              : launch_steps<DT, S, 1>(p, blocks, bn, stream);
 }
 
 template <int DT>
 hipError_t launch_outer_dt(Prod p, hipStream_t stream) {
     constexpr int KS = Step<DT>::K;
-    p.cvec = epilogue_vec(p, (int)sizeof(typename Type<DT>::T));
-    if (p.K <= KS) return launch_steps<DT, 1>(p, stream);
-    if (DT != SGEMM_DTYPE_F32 || p.K <= 2 * KS) return launch_steps<DT, 2>(p, stream);
-    return launch_steps<DT, DT == SGEMM_DTYPE_F32 ? 4 : 2>(p, stream);
+    if (p.K <= KS) return launch_split<DT, 1>(p, stream);
+    if (DT != SGEMM_DTYPE_F32 || p.K <= 2 * KS) return launch_split<DT, 2>(p, stream);
+    return launch_split<DT, DT == SGEMM_DTYPE_F32 ? 4 : 2>(p, stream);
 }
 
 }  // namespace

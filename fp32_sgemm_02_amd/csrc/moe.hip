@@ -428,7 +428,6 @@ __global__ void __launch_bounds__(64 * NW) down_kernel(Moe m, MoeWs s) {
     if (!arrive_last(s.joined + blockIdx.x, s.routing->active, last)) return;
     const int tid = threadIdx.x;
     Prod p{m.T, m.D, 0, nullptr, 0, nullptr, 0, m.Y, m.ldy};
-    p.cvec = rows16(m.Y, m.ldy, (int)sizeof(typename Type<DT>::T));
     for (int q = tid; q < m.T * 8; q += 64 * NW) {
         const int t = q >> 3, d = d0 + 4 * (q & 7);
         if (d >= m.D) continue;

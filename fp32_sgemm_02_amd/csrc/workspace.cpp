@@ -25,12 +25,22 @@
 // counters cleared by a recorded fill kernel), so replays of the graph never
 // share memory with eager calls.
 //
+// The feed-forward operators' buffers (kind 1) are different under capture: an
+// ordinary allocation, made in relaxed capture mode, shared by the calls that one
+// capture records on one stream (they run in order) and by no other graph, and
+// kept until sgemm_workspace_release or the end of the process.  Their calls
+// are many to a graph, and graphs that held several allocation nodes each were
+// not executed at all on replay once other such graphs were alive (a step of
+// four fp32 calls, four graphs: the second and fourth left their results as they
+// were, with no error).
+//
 // A problem that brings its own scratch (Problem::scratch, set by the entry
 // point that allocates nothing) takes it instead, with no allocation at all.
 #include <map>
 #include <mutex>
 #include <thread>
 #include <tuple>
+#include <vector>
 
 #include "gemm_internal.hpp"
 
@@ -62,6 +72,15 @@ struct Cached {
 
 using Key = std::tuple<int, hipStream_t, std::thread::id, int>;
 
+// (device, stream, capture): the buffers of one capture's calls, the last the
+// largest (earlier ones belong to nodes that are recorded already).
+using CaptureKey = std::tuple<int, hipStream_t, unsigned long long>;
+
+std::map<CaptureKey, std::vector<Cached>> &captured() {
+    static std::map<CaptureKey, std::vector<Cached>> c;
+    return c;
+}
+
 std::mutex &cache_mutex() {
     static std::mutex m;
     return m;
@@ -77,6 +96,41 @@ void fill(Workspace &w, void *base, bool owned) {
     w.counters = static_cast<unsigned *>(base);
     w.ptr = static_cast<unsigned char *>(base) + kWorkspaceCounterBytes;
     w.owned = owned;
+}
+
+// The buffer of a capture on `stream`; its counters are cleared by a recorded
+// kernel when it is new.
+hipError_t captured_buffer(size_t bytes, hipStream_t stream, Workspace &w) {
+    hipStreamCaptureStatus status;
+    unsigned long long id = 0;
+    hipError_t e = hipStreamGetCaptureInfo(stream, &status, &id);
+    if (e != hipSuccess) return e;
+    int dev = 0;
+    e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    std::lock_guard<std::mutex> lock(cache_mutex());
+    std::vector<Cached> &own = captured()[CaptureKey{dev, stream, id}];
+    if (own.empty() || own.back().bytes < bytes) {
+        // (an allocation is not stream work: relaxed mode lets the capture go on)
+        hipStreamCaptureMode mode = hipStreamCaptureModeRelaxed;
+        e = hipThreadExchangeStreamCaptureMode(&mode);
+        if (e != hipSuccess) return e;
+        void *base = nullptr;
+        const hipError_t got = hipMalloc(&base, bytes + kWorkspaceCounterBytes);
+        e = hipThreadExchangeStreamCaptureMode(&mode);
+        if (got != hipSuccess) return got;
+        if (e == hipSuccess) e = clear_counters(base, stream);
+        if (e != hipSuccess) {
+            (void)hipFree(base);   // the first error is the one reported
+            return e;
+        }
+        Cached c;
+        c.ptr = base;
+        c.bytes = bytes;
+        own.push_back(c);
+    }
+    fill(w, own.back().ptr, false);
+    return hipSuccess;
 }
 
 }  // namespace
@@ -114,6 +168,7 @@ hipError_t workspace_acquire(size_t bytes, hipStream_t stream, const Problem &p,
     hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
     hipError_t e = hipStreamIsCapturing(stream, &cap);
     if (e != hipSuccess) return e;
+    if (cap != hipStreamCaptureStatusNone && kind != 0) return captured_buffer(bytes, stream, w);
     if (cap != hipStreamCaptureStatusNone) {
         void *base = nullptr;
         e = hipMallocAsync(&base, bytes + kWorkspaceCounterBytes, stream);
@@ -165,6 +220,17 @@ hipError_t workspace_release_all() {
             const hipError_t f = hipFreeAsync(it->second.ptr, nullptr);
             if (f != hipSuccess && e == hipSuccess) e = f;
             it = cache().erase(it);
+        } else {
+            ++it;
+        }
+    }
+    for (auto it = captured().begin(); it != captured().end();) {
+        if (std::get<0>(it->first) == dev) {
+            for (const Cached &c : it->second) {
+                const hipError_t f = hipFree(c.ptr);
+                if (f != hipSuccess && e == hipSuccess) e = f;
+            }
+            it = captured().erase(it);
         } else {
             ++it;
         }
