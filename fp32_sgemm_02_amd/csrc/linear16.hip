@@ -160,6 +160,32 @@ struct Operand {
     }
 };
 
+// Copies of operands whose rows do not take direct loads, with rows of whole
+// 16-byte chunks (the fill is zeros): one launch for both operands, blockIdx.y.
+struct Pack {
+    const u16 *src[2];
+    u16 *dst[2];
+    long long ld[2];
+    int rows[2], cols[2], chunks[2];   // chunks: 8-value chunks of a row
+};
+
+__global__ void __launch_bounds__(256) pack_kernel(Pack p) {
+    const int o = blockIdx.y, chunks = p.chunks[o];
+    const long long total = (long long)p.rows[o] * chunks;
+    for (long long q = blockIdx.x * 256ll + threadIdx.x; q < total; q += gridDim.x * 256ll) {
+        const int r = (int)(q / chunks), c = 8 * (int)(q % chunks), n = p.cols[o] - c;
+        const u16 *s = p.src[o] + r * p.ld[o] + c;
+        uintx4 v = {0, 0, 0, 0};
+        if (n >= 8)
+            __builtin_memcpy(&v, s, 16);
+        else
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < n) v[e / 2] |= (unsigned)s[e] << (16 * (e & 1));
+        *reinterpret_cast<uintx4 *>(p.dst[o] + q * 8) = v;
+    }
+}
+
 struct Grid16 {
     int tiles_m, tiles_n, group_m;
     int slices, per;     // k slices, stages per slice
@@ -333,10 +359,18 @@ bool direct_ok(const void *q, long long ld, int row_len, int bt, int mc) {
     return rows16(q, ld, 2) && row_len % 8 == 0 && (mc ? kBK : bt) * ld * 2 < 0x7fff0000LL;
 }
 
+// Whether p's operands are loaded directly by tiles of bt rows.
+bool a_direct(const Prod &p, int bt) {
+    return direct_ok(p.A, p.lda, p.a_pad ? 0 : p.a_mc ? p.M : p.K, bt, p.a_mc);
+}
+bool b_direct(const Prod &p, int bt) {
+    return direct_ok(p.B, p.ldb, p.b_pad ? 0 : p.b_mc ? p.N : p.K, bt, p.b_mc);
+}
+
 struct Plan16 {
     int bm, bn, slices, per;
     bool brief;   // one or two stages: a ring of two, so that more tiles share a CU
-    bool big;   // linear16_big.hip
+    bool big;     // linear16_big.hip
 };
 
 constexpr int kCUs = 256;
@@ -344,13 +378,14 @@ constexpr int kCUs = 256;
 Plan16 plan16(const Prod &p) {
     auto tiles = [&](int b) { return (long long)((p.M + b - 1) / b) * ((p.N + b - 1) / b); };
     Plan16 q{};
-    q.big = tiles(256) >= kCUs / 2 &&
-            direct_ok(p.A, p.lda, p.a_pad ? 0 : p.a_mc ? p.M : p.K, 256, p.a_mc) &&
-            direct_ok(p.B, p.ldb, p.b_mc ? p.N : p.K, 256, p.b_mc);
+    q.big = tiles(256) >= kCUs / 2 && a_direct(p, 256) && b_direct(p, 256);
     q.bm = q.bn = tiles(128) >= kCUs ? 128 : 64;
     const long long t = tiles(q.bm);
     const int stages = (p.K + kBK - 1) / kBK;
     int s = 1;
+    // split k where tiles leave half the CUs without work (with more tiles the
+    // partial sums' way through memory costs more than it gains: 2048^3 24 us
+    // whole, 42 in two)
     if (!q.big && t <= kCUs / 2) {
         s = (int)(kCUs / t);
         const int most = stages / 4;
@@ -362,6 +397,42 @@ Plan16 plan16(const Prod &p) {
     q.per = (stages + s - 1) / s;
     if (q.per < 1) q.per = 1;
     q.slices = stages ? (stages + q.per - 1) / q.per : 1;
+    return q;
+}
+
+// Operands that the tiles cannot load directly are copied first where the
+// product is large enough to pay for it (the register path reaches a third of
+// the rate: 4096 x 4096 x 4097 bf16 PACK_FIG; at 2 GFLOP the copy's launch takes
+// what it saves).  Returns p as the tiles see it, with the copies in `at`, and the
+// bytes they take.
+Prod packed(const Prod &p, unsigned char *at, Pack *pack, size_t *bytes) {
+    Prod q = p;
+    *bytes = 0;
+    if (pack) *pack = Pack{};
+    if (2.0 * p.M * p.N * p.K < 2e9) return q;
+    auto take = [&](int o, const void *&X, long long &ld, int rows, int cols) {
+        const int chunks = (cols + 7) / 8;
+        u16 *dst = reinterpret_cast<u16 *>(at + *bytes);
+        if (pack) {
+            pack->src[o] = static_cast<const u16 *>(X);
+            pack->dst[o] = dst;
+            pack->ld[o] = ld;
+            pack->rows[o] = rows;
+            pack->cols[o] = cols;
+            pack->chunks[o] = chunks;
+        }
+        X = dst;
+        ld = 8ll * chunks;
+        *bytes += ((size_t)rows * chunks * 16 + 255) / 256 * 256;
+    };
+    if (!a_direct(p, 256)) {
+        take(0, q.A, q.lda, p.a_mc ? p.K : p.M, p.a_mc ? p.M : p.K);
+        q.a_pad = 1;
+    }
+    if (!b_direct(p, 256)) {
+        take(1, q.B, q.ldb, p.b_mc ? p.K : p.N, p.b_mc ? p.N : p.K);
+        q.b_pad = 1;
+    }
     return q;
 }
 
@@ -390,7 +461,15 @@ hipError_t launch_layout(const Prod &p, const Grid16 &gr, bool ad, bool bd, hipS
 }
 
 template <int DT>
-hipError_t launch_dt(Prod p, const Workspace &ws, hipStream_t stream) {
+hipError_t launch_dt(const Prod &given, const Workspace &ws, hipStream_t stream) {
+    Pack pack;
+    size_t bytes = 0;
+    const Prod p = packed(given, static_cast<unsigned char *>(ws.ptr), &pack, &bytes);
+    if (bytes) {
+        hipLaunchKernelGGL(pack_kernel, dim3(2 * kCUs, 2), dim3(256), 0, stream, pack);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
     const Plan16 q = plan16(p);
     if (q.big) return launch_prod16_big(DT, p, stream);
     Grid16 gr{};
@@ -399,10 +478,9 @@ hipError_t launch_dt(Prod p, const Workspace &ws, hipStream_t stream) {
     gr.group_m = 8;
     gr.slices = q.slices;
     gr.per = q.per;
-    gr.part = static_cast<float *>(ws.ptr);
+    gr.part = reinterpret_cast<float *>(static_cast<unsigned char *>(ws.ptr) + bytes);
     gr.count = ws.counters;
-    const bool ad = direct_ok(p.A, p.lda, p.a_pad ? 0 : p.a_mc ? p.M : p.K, q.bm, p.a_mc);
-    const bool bd = direct_ok(p.B, p.ldb, p.b_mc ? p.N : p.K, q.bn, p.b_mc);
+    const bool ad = a_direct(p, q.bm), bd = b_direct(p, q.bm);
     if (q.bm == 128)
         return q.brief ? launch_layout<DT, 128, 128, 64, 64, 2, 2>(p, gr, ad, bd, stream)
                        : launch_layout<DT, 128, 128, 64, 64, 4, 2>(p, gr, ad, bd, stream);
@@ -412,11 +490,14 @@ hipError_t launch_dt(Prod p, const Workspace &ws, hipStream_t stream) {
 
 }  // namespace
 
-size_t prod16_workspace(int, const Prod &p) {
+size_t prod16_workspace(int, const Prod &given) {
+    size_t bytes = 0;
+    // (copies lie on 256-byte boundaries, as at this address)
+    const Prod p = packed(given, reinterpret_cast<unsigned char *>(4096), nullptr, &bytes);
     const Plan16 q = plan16(p);
-    if (q.slices == 1) return 0;
+    if (q.slices == 1) return bytes;
     const size_t tiles = (size_t)((p.M + q.bm - 1) / q.bm) * ((p.N + q.bn - 1) / q.bn);
-    return tiles * q.slices * q.bm * q.bn * sizeof(float);
+    return bytes + tiles * q.slices * q.bm * q.bn * sizeof(float);
 }
 
 hipError_t launch_prod16(int dtype, const Prod &p, const Workspace &ws, hipStream_t stream) {

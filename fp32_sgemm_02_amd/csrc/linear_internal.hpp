@@ -34,7 +34,7 @@ struct Prod {
     void *Z = nullptr;
     long long ldz = 0;
     int act = SGEMM_ACT_NONE;
-    int a_pad = 0;  // the rows of A are filled up with zeros to 16 bytes
+    int a_pad = 0, b_pad = 0;   // the stored rows are filled up with zeros to 16 bytes
     // What the rounding of A left over, laid out as A (few-rows kernels only).
     const void *lo = nullptr;
 };
