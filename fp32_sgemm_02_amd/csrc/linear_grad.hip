@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(256) grad_kernel(GradArgs a) {
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 float v = Ty::load(y[e]);
-                if (ACT != SGEMM_ACT_NONE) v *= slope_t<ACT>(Ty::load(x[e]));
+                if (ACT != SGEMM_ACT_NONE) v *= slope_for<DT, ACT>(Ty::load(x[e]));
                 sum[e] += v;
                 o[e] = Ty::store(v);
                 // what the rounding of G left over; 0 where G overflowed
