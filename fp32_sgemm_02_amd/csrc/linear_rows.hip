@@ -222,12 +222,15 @@ __global__ void __launch_bounds__(64 * NW) cols_kernel(Prod p, RowsGrid gr) {
         }
 #pragma unroll
         for (int e = 0; e < V; ++e)
-            r.w[e] = load_frag<DT>(B + (long long)(kg + e) * p.ldb, kg + e < ke ? cols : 0);
+            r.w[e] = load_frag<DT>(B + (long long)(kg + e) * p.ldb, kg + e < ke ? cols : 0, Bf);
 #pragma unroll
         for (int t = 0; t < TB; ++t) {
             const long long at = (long long)min(16 * t + i, p.M - 1) * p.lda + kg;
-            r.x[t] = load_frag<DT>(static_cast<const T *>(p.A) + at, ke - kg);
-            if constexpr (LO) r.l[t] = load_frag<DT>(static_cast<const T *>(p.lo) + at, ke - kg);
+            r.x[t] = load_frag<DT>(static_cast<const T *>(p.A) + at, ke - kg,
+                                   static_cast<const T *>(p.A));
+            if constexpr (LO)
+                r.l[t] = load_frag<DT>(static_cast<const T *>(p.lo) + at, ke - kg,
+                                       static_cast<const T *>(p.lo));
         }
     };
     floatx4 acc[V][TB];
@@ -352,6 +355,13 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(Prod p, int blocks_n) {
                 if constexpr (LO)
                     a[1][e] = load_whole<DT>(static_cast<const T *>(p.lo) + kc * p.lda + amf, in);
             }
+        } else if (p.K == 0) {   // no row to read: dW is zero
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                b[e] = uintx4{0, 0, 0, 0};
+#pragma unroll
+                for (int q = 0; q < PARTS; ++q) a[q][e] = uintx4{0, 0, 0, 0};
+            }
         } else {
 #pragma unroll
             for (int e = 0; e < V; ++e) {
@@ -359,10 +369,12 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(Prod p, int blocks_n) {
                 const bool in = k < p.K;
                 const long long at = (long long)k * p.lda + am;
                 b[e] = load_frag<DT>(static_cast<const T *>(p.B) + (long long)k * p.ldb + bn,
-                                     in ? p.N - bn : 0);
-                a[0][e] = load_frag<DT>(static_cast<const T *>(p.A) + at, in ? p.M - am : 0);
+                                     in ? p.N - bn : 0, static_cast<const T *>(p.B));
+                a[0][e] = load_frag<DT>(static_cast<const T *>(p.A) + at, in ? p.M - am : 0,
+                                        static_cast<const T *>(p.A));
                 if constexpr (LO)
-                    a[1][e] = load_frag<DT>(static_cast<const T *>(p.lo) + at, in ? p.M - am : 0);
+                    a[1][e] = load_frag<DT>(static_cast<const T *>(p.lo) + at, in ? p.M - am : 0,
+                                            static_cast<const T *>(p.lo));
             }
         }
 #pragma unroll

@@ -80,9 +80,9 @@ __global__ void __launch_bounds__(kThreads) router_kernel(Moe m, MoeWs s) {
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const int d = d0 + u * 64 * V;
-                    a[u] = load_frag<DT>(x + d, m.D - d);
+                    a[u] = load_frag<DT>(x + d, m.D - d, x);
 #pragma unroll
-                    for (int q = 0; q < EPW; ++q) b[u][q] = load_frag<DT>(w[q] + d, m.D - d);
+                    for (int q = 0; q < EPW; ++q) b[u][q] = load_frag<DT>(w[q] + d, m.D - d, w[q]);
                 }
             }
 #pragma unroll

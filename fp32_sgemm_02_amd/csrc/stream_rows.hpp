@@ -31,23 +31,23 @@ __device__ __forceinline__ floatx4 mfma_step(uintx4 w, uintx4 x, floatx4 c) {
 }
 
 // V values from p on, of which n lie inside (zeros for the others, which are
-// not read).  Rows may start at any multiple of the value's size: the target
-// loads 16 bytes from any address.
+// not read; n <= 0: none).  `safe`: any readable value.  Branch-free: loads behind
+// per-lane branches wait for one another, and a tail of a few chunks then takes
+// longer than the rows before it (16 x 4097 x 4097 bf16 42 us, FRAG_FIG so).
 template <int DT>
-__device__ __forceinline__ uintx4 load_frag(const typename Type<DT>::T *p, int n) {
+__device__ __forceinline__ uintx4 load_frag(const typename Type<DT>::T *p, int n,
+                                            const typename Type<DT>::T *safe) {
     constexpr int V = Type<DT>::V;
-    uintx4 v = {0, 0, 0, 0};
-    if (n >= V) {
-        __builtin_memcpy(&v, p, 16);
-    } else {
+    typename Type<DT>::T t[V];
 #pragma unroll
-        for (int e = 0; e < V; ++e)
-            if (e < n) {
-                if constexpr (DT == SGEMM_DTYPE_F32)
-                    v[e] = __builtin_bit_cast(unsigned, p[e]);
-                else
-                    v[e / 2] |= (unsigned)p[e] << (16 * (e & 1));
-            }
+    for (int e = 0; e < V; ++e) t[e] = *(e < n ? p + e : safe);
+    uintx4 v = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        if constexpr (DT == SGEMM_DTYPE_F32)
+            v[e] = e < n ? __builtin_bit_cast(unsigned, t[e]) : 0u;
+        else
+            v[e / 2] |= e < n ? (unsigned)t[e] << (16 * (e & 1)) : 0u;
     }
     return v;
 }
@@ -83,18 +83,31 @@ __device__ __forceinline__ void stream_dot(const typename Type<DT>::T *const (&w
             for (int u = 0; u < U; ++u) {
                 const int kk = k + u * KS + kg;
 #pragma unroll
-                for (int q = 0; q < RB; ++q) __builtin_memcpy(&r.w[u][q], w[q] + kk, 16);
+                for (int q = 0; q < RB; ++q) r.w[u][q] = load_whole<DT>(w[q] + kk);
 #pragma unroll
-                for (int q = 0; q < TB; ++q) __builtin_memcpy(&r.x[u][q], x[q] + kk, 16);
+                for (int q = 0; q < TB; ++q) r.x[u][q] = load_whole<DT>(x[q] + kk);
             }
-        } else {
+            return;
+        }
+        // the last round: whole steps, one that ends inside, and none
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int kk = k + u * KS + kg;
+        for (int u = 0; u < U; ++u) {
+            const int ku = k + u * KS, kk = ku + kg;
+            if (ku + KS <= k1) {
 #pragma unroll
-                for (int q = 0; q < RB; ++q) r.w[u][q] = load_frag<DT>(w[q] + kk, k1 - kk);
+                for (int q = 0; q < RB; ++q) r.w[u][q] = load_whole<DT>(w[q] + kk);
 #pragma unroll
-                for (int q = 0; q < TB; ++q) r.x[u][q] = load_frag<DT>(x[q] + kk, k1 - kk);
+                for (int q = 0; q < TB; ++q) r.x[u][q] = load_whole<DT>(x[q] + kk);
+            } else if (ku < k1) {
+#pragma unroll
+                for (int q = 0; q < RB; ++q) r.w[u][q] = load_frag<DT>(w[q] + kk, k1 - kk, w[q]);
+#pragma unroll
+                for (int q = 0; q < TB; ++q) r.x[u][q] = load_frag<DT>(x[q] + kk, k1 - kk, x[q]);
+            } else {
+#pragma unroll
+                for (int q = 0; q < RB; ++q) r.w[u][q] = uintx4{0, 0, 0, 0};
+#pragma unroll
+                for (int q = 0; q < TB; ++q) r.x[u][q] = uintx4{0, 0, 0, 0};
             }
         }
     };
