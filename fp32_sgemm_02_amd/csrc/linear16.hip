@@ -402,14 +402,15 @@ Plan16 plan16(const Prod &p) {
 
 // Operands that the tiles cannot load directly are copied first where the
 // product is large enough to pay for it (the register path reaches a third of
-// the rate: 4096 x 4096 x 4097 bf16 284 us, 135 with the copies; at 2 GFLOP the copy's launch takes
-// what it saves).  Returns p as the tiles see it, with the copies in `at`, and the
+// the rate: 4096 x 4096 x 4097 bf16 284 us, 135 with the copies; smaller ones
+// lose more by the copies' launch than they gain: 1000 x 3001 x 777 18 us without
+// and 23 with them, but 44 and 30 where W is read transposed).  Returns p as the tiles see it, with the copies in `at`, and the
 // bytes they take.
 Prod packed(const Prod &p, unsigned char *at, Pack *pack, size_t *bytes) {
     Prod q = p;
     *bytes = 0;
     if (pack) *pack = Pack{};
-    if (2.0 * p.M * p.N * p.K < 2e9) return q;
+    if (2.0 * p.M * p.N * p.K < (p.b_mc ? 2e9 : 8e9)) return q;
     auto take = [&](int o, const void *&X, long long &ld, int rows, int cols) {
         const int chunks = (cols + 7) / 8;
         u16 *dst = reinterpret_cast<u16 *>(at + *bytes);

@@ -231,6 +231,30 @@ typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef unsigned uintx4 __attribute__((ext_vector_type(4)));
 typedef unsigned uintx2 __attribute__((ext_vector_type(2)));
 
+// 16 bytes from any place where a value may start.  16-bit values that start in
+// the middle of a dword are put together from the five aligned dwords that hold
+// them (the hardware loads 16 bytes from any address, but slowly unless it is a
+// dword's: 16 x 4097 x 4097 bf16 40 us, 26 so; the tile kernel's register path gains
+// nothing by it).  Each of those dwords holds a value
+// of the sixteen bytes, so none lies outside the array's memory pages.
+template <int DT>
+__device__ __forceinline__ uintx4 load_any(const typename Type<DT>::T *p) {
+    uintx4 v;
+    if constexpr (DT == SGEMM_DTYPE_F32) {
+        __builtin_memcpy(&v, p, 16);
+    } else {
+        const unsigned mis = (unsigned)(unsigned long long)p & 2u;
+        const unsigned *q = reinterpret_cast<const unsigned *>(
+            reinterpret_cast<unsigned long long>(p) & ~3ull);
+        __builtin_memcpy(&v, q, 16);
+        const unsigned e = q[mis ? 4 : 3];
+        const unsigned s = 8 * mis;
+        v = uintx4{__builtin_amdgcn_alignbit(v[1], v[0], s), __builtin_amdgcn_alignbit(v[2], v[1], s),
+                   __builtin_amdgcn_alignbit(v[3], v[2], s), __builtin_amdgcn_alignbit(e, v[3], s)};
+    }
+    return v;
+}
+
 // D += A B over 32 k values of 16-bit inputs.  Lane (i, g) = (lane % 16,
 // lane / 16): a holds A(row i, k = 8g .. 8g+7), b holds B(column i, same k),
 // and c holds D(rows 4g .. 4g+3, column i).

@@ -33,7 +33,7 @@ __device__ __forceinline__ floatx4 mfma_step(uintx4 w, uintx4 x, floatx4 c) {
 // V values from p on, of which n lie inside (zeros for the others, which are
 // not read; n <= 0: none).  `safe`: any readable value.  Branch-free: loads behind
 // per-lane branches wait for one another, and a tail of a few chunks then takes
-// longer than the rows before it (16 x 4097 x 4097 bf16 42 us, FRAG_FIG so).
+// longer than the rows before it.
 template <int DT>
 __device__ __forceinline__ uintx4 load_frag(const typename Type<DT>::T *p, int n,
                                             const typename Type<DT>::T *safe) {
@@ -83,9 +83,9 @@ __device__ __forceinline__ void stream_dot(const typename Type<DT>::T *const (&w
             for (int u = 0; u < U; ++u) {
                 const int kk = k + u * KS + kg;
 #pragma unroll
-                for (int q = 0; q < RB; ++q) r.w[u][q] = load_whole<DT>(w[q] + kk);
+                for (int q = 0; q < RB; ++q) r.w[u][q] = load_any<DT>(w[q] + kk);
 #pragma unroll
-                for (int q = 0; q < TB; ++q) r.x[u][q] = load_whole<DT>(x[q] + kk);
+                for (int q = 0; q < TB; ++q) r.x[u][q] = load_any<DT>(x[q] + kk);
             }
             return;
         }
@@ -95,9 +95,9 @@ __device__ __forceinline__ void stream_dot(const typename Type<DT>::T *const (&w
             const int ku = k + u * KS, kk = ku + kg;
             if (ku + KS <= k1) {
 #pragma unroll
-                for (int q = 0; q < RB; ++q) r.w[u][q] = load_whole<DT>(w[q] + kk);
+                for (int q = 0; q < RB; ++q) r.w[u][q] = load_any<DT>(w[q] + kk);
 #pragma unroll
-                for (int q = 0; q < TB; ++q) r.x[u][q] = load_whole<DT>(x[q] + kk);
+                for (int q = 0; q < TB; ++q) r.x[u][q] = load_any<DT>(x[q] + kk);
             } else if (ku < k1) {
 #pragma unroll
                 for (int q = 0; q < RB; ++q) r.w[u][q] = load_frag<DT>(w[q] + kk, k1 - kk, w[q]);
