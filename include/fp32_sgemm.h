@@ -416,11 +416,15 @@ int sgemm_workspace_release(void);
  * Intermediate values live in a workspace of their own per device and stream
  * (per host thread for the per-thread default stream), grown when a call needs
  * more and released by sgemm_workspace_release: an M x N array for a backward
- * pass with an activation and for the fp32 linear layer with a residual of
- * more than 64 rows; partial sums of products split over their inner length;
- * for the experts T * top_k * (F + D) values.  Under graph capture it is the
- * graph's own, as for the products.  The launches of a call are made together:
- * host threads that share a stream do not interleave them.
+ * pass with an activation (two for at most 64 rows of 16-bit types) and for an
+ * fp32 linear layer with a residual that no fused tile serves; copies of 16-bit
+ * operands whose rows do not start on 16 bytes, for large products; partial sums
+ * of products split over their inner length; for the experts T * top_k * (F +
+ * D) floats.  Under graph capture the calls that one capture records on one
+ * stream share an allocation of that capture's own, which lives until
+ * sgemm_workspace_release or the end of the process: a graph must not be
+ * replayed after that call.  The launches of a call are made together: host
+ * threads that share a stream do not interleave them.
  */
 
 /*
