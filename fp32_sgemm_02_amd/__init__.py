@@ -497,6 +497,8 @@ def _matrix(name, t, rows, cols, dtype, dev):
         if r > 1 and c > 0:
             raise ValueError(f"{name}: rows must not overlap")
         ld = c if c > 1 else 1
+    if ld > 0x7fffffff or r > 0x7fffffff:
+        raise ValueError(f"{name}: sizes and strides must fit 32 bits")
     return t.data_ptr() or None, ld
 
 
@@ -620,6 +622,8 @@ def _stack(name, t, n, rows, cols, dtype, dev):
     step, ld, one = t.stride()
     if one != 1 and cols > 1:
         raise ValueError(f"{name}: rows must be contiguous (stride(2) == 1)")
+    if ld > 0x7fffffff:
+        raise ValueError(f"{name}: strides must fit 32 bits")
     return t.data_ptr() or None, ld if rows > 1 else max(ld, cols), step if n > 1 else 0
 
 

@@ -8,6 +8,7 @@
 // together in the stream's order.
 #include <cstdint>
 #include <mutex>
+#include <new>
 
 #include "linear_internal.hpp"
 
@@ -29,6 +30,19 @@ size_t round_up(size_t v, size_t to) { return (v + to - 1) / to * to; }
 std::mutex &launch_mutex() {
     static std::mutex m;
     return m;
+}
+
+// f's status; a C++ exception (host memory, a mutex) becomes one, since none may
+// cross the C interface.
+template <class F>
+int guarded(F &&f) {
+    try {
+        return f();
+    } catch (const std::bad_alloc &) {
+        return to_status(hipErrorOutOfMemory);
+    } catch (...) {
+        return to_status(hipErrorUnknown);
+    }
 }
 
 // The feed-forward workspace of a call: acquired (where bytes are needed),
@@ -242,7 +256,7 @@ int sgemm_linear(int dtype, int M, int N, int K, const void *X, int ldx, const v
     p.Z = Z;
     p.ldz = ldz;
     p.act = act;
-    return run_linear(dtype, p, stream);
+    return guarded([&] { return run_linear(dtype, p, stream); });
 }
 
 int sgemm_linear_backward(int dtype, int M, int N, int K, const void *dY, int lddy, const void *Z,
@@ -271,7 +285,7 @@ int sgemm_linear_backward(int dtype, int M, int N, int K, const void *dY, int ld
     if (dW && lddw < k1) return bad(17);
     if (db && !aligned(db, elem)) return bad(18);
     const Backward b{M, N, K, dY, lddy, Z, ldz, act, X, ldx, W, ldw, dX, lddx, dW, lddw, db};
-    return run_backward(dtype, b, stream);
+    return guarded([&] { return run_backward(dtype, b, stream); });
 }
 
 int sgemm_moe(int dtype, int T, int D, int F, int E, int top_k, int gated, int renormalize, int act,
@@ -306,8 +320,10 @@ int sgemm_moe(int dtype, int T, int D, int F, int E, int top_k, int gated, int r
     if (!usable(Y, elem)) return bad(20);
     const Moe m{T,  D,   F,   E,       top_k, gated, renormalize, act,     X, ldx, Wr, ldr,
                 W1, ld1, stride1, W2,  ld2,   stride2, Y,         ldy, ids, weights};
-    return with_workspace(moe_workspace(dtype, m), true, stream, [&](const Workspace &ws) {
-        return to_status(launch_moe(dtype, m, ws, stream));
+    return guarded([&] {
+        return with_workspace(moe_workspace(m), true, stream, [&](const Workspace &ws) {
+            return to_status(launch_moe(dtype, m, ws, stream));
+        });
     });
 }
 

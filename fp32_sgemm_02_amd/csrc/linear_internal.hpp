@@ -88,7 +88,7 @@ struct Moe {
     int *ids;         // T x k, or null
     float *weights;   // T x k, or null
 };
-size_t moe_workspace(int dtype, const Moe &m);
+size_t moe_workspace(const Moe &m);
 hipError_t launch_moe(int dtype, const Moe &m, const Workspace &ws, hipStream_t stream);
 
 // Y = act(Z) + R elementwise over M x N in fp32, in place where Y is Z.

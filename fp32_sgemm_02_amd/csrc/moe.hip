@@ -457,8 +457,8 @@ __global__ void __launch_bounds__(64 * NW) down_kernel(Moe m, MoeWs s) {
 size_t round_up(size_t v, size_t to) { return (v + to - 1) / to * to; }
 
 // The workspace's parts, in order; returns the bytes.
-size_t lay_out(int dtype, const Moe &m, const Workspace *ws, MoeWs &s) {
-    const size_t elem = dtype == SGEMM_DTYPE_F32 ? 4 : 2, P = (size_t)m.T * m.k;
+size_t lay_out(const Moe &m, const Workspace *ws, MoeWs &s) {
+    const size_t P = (size_t)m.T * m.k;
     s.fp = (int)round_up(m.F, 16);
     s.dp = (int)round_up(m.D, 16);
     size_t at = 0;
@@ -473,7 +473,6 @@ size_t lay_out(int dtype, const Moe &m, const Workspace *ws, MoeWs &s) {
     s.routing = reinterpret_cast<Routing *>(take(sizeof(Routing)));
     s.h = take(P * s.fp * 4);   // two parts of 2 bytes, or one of 4
     s.part = reinterpret_cast<float *>(take(P * s.dp * 4));
-    (void)elem;
     s.routed = ws ? ws->counters : nullptr;
     s.chosen = ws ? ws->counters + kMoeTokens : nullptr;
     s.joined = ws ? ws->counters + kMoeTokens + 1 : nullptr;
@@ -530,14 +529,14 @@ hipError_t launch_dt(const Moe &m, const MoeWs &s, hipStream_t stream) {
 
 }  // namespace
 
-size_t moe_workspace(int dtype, const Moe &m) {
+size_t moe_workspace(const Moe &m) {
     MoeWs s;
-    return lay_out(dtype, m, nullptr, s);
+    return lay_out(m, nullptr, s);
 }
 
 hipError_t launch_moe(int dtype, const Moe &m, const Workspace &ws, hipStream_t stream) {
     MoeWs s;
-    lay_out(dtype, m, &ws, s);
+    lay_out(m, &ws, s);
     switch (dtype) {
     case SGEMM_DTYPE_BF16: return launch_dt<SGEMM_DTYPE_BF16>(m, s, stream);
     case SGEMM_DTYPE_F16: return launch_dt<SGEMM_DTYPE_F16>(m, s, stream);

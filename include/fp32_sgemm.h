@@ -423,7 +423,8 @@ int sgemm_workspace_release(void);
  * D) floats.  Under graph capture the calls that one capture records on one
  * stream share an allocation of that capture's own, which lives until
  * sgemm_workspace_release or the end of the process: a graph must not be
- * replayed after that call.  The launches of a call are made together: host
+ * replayed after that call, and two executables of one captured graph must
+ * not run at once.  The launches of a call are made together: host
  * threads that share a stream do not interleave them.
  */
 
