@@ -163,9 +163,11 @@ int run_backward(int dtype, const Backward &b, hipStream_t stream) {
     const size_t g_bytes =
         make_g ? round_up((size_t)(two ? 2 : 1) * b.M * ldg * elem, 256) : 0;
 
-    Prod dx{b.M, b.K, b.N, b.dY, ldg, b.W, b.ldw, b.dX, b.lddx};
+    // (plans are made before G has its place: as well aligned as this)
+    const void *g_at = make_g ? reinterpret_cast<const void *>(uintptr_t{4096}) : b.dY;
+    Prod dx{b.M, b.K, b.N, g_at, ldg, b.W, b.ldw, b.dX, b.lddx};
     dx.b_mc = 1;
-    Prod dw{b.N, b.K, b.M, b.dY, ldg, b.X, b.ldx, b.dW, b.lddw};
+    Prod dw{b.N, b.K, b.M, g_at, ldg, b.X, b.ldx, b.dW, b.lddw};
     dw.a_mc = dw.b_mc = 1;
     dx.a_pad = dw.a_pad = make_g;
     const bool dx_ours = want_dx && (!f32 || few), dw_ours = want_dw && (!f32 || few);
@@ -176,9 +178,7 @@ int run_backward(int dtype, const Backward &b, hipStream_t stream) {
         q.trans_a = ta;
         return q;
     };
-    // fp32 products of more than a few rows run as the library's own (the address
-    // of G, when it is made, is as well aligned as any)
-    const void *g_at = make_g ? reinterpret_cast<const void *>(uintptr_t{4096}) : b.dY;
+    // fp32 products of more than a few rows run as the library's own
     Problem dx32 = op32(0, b.M, b.K, b.N, g_at, ldg, b.W, b.ldw, b.dX, b.lddx);
     Problem dw32 = op32(1, b.N, b.K, b.M, g_at, ldg, b.X, b.ldx, b.dW, b.lddw);
     const bool dx_lib = want_dx && !dx_ours, dw_lib = want_dw && !dw_ours;
@@ -193,6 +193,8 @@ int run_backward(int dtype, const Backward &b, hipStream_t stream) {
         const size_t s = ours_workspace(dtype, dw, false);
         if (s > scratch) scratch = s;
     }
+    const bool pair = dx_ours && dw_ours && !few;   // 16-bit, more than a few rows
+    if (pair && prod16_pair_workspace(dx, dw) > scratch) scratch = prod16_pair_workspace(dx, dw);
     // the workspace: the launches' partial sums, one after another's, then G
     scratch = round_up(scratch, 256);
     return with_workspace(scratch + g_bytes, false, stream, [&](const Workspace &ws) -> int {
@@ -210,6 +212,7 @@ int run_backward(int dtype, const Backward &b, hipStream_t stream) {
             }
             dx.lo = dw.lo = lo;
         }
+        if (pair) return to_status(launch_prod16_pair(dtype, dx, dw, ws, stream));
         if (want_dx) {
             const int st = dx_lib ? run_in(dx32, ws, scratch, stream)
                                   : to_status(launch_product(dtype, dx, few, ws, stream));

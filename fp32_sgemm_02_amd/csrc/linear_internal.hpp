@@ -45,6 +45,12 @@ struct Prod {
 size_t prod16_workspace(int dtype, const Prod &p);
 hipError_t launch_prod16(int dtype, const Prod &p, const Workspace &ws, hipStream_t stream);
 
+// dX and dW of one backward pass (a_mc 0 and 1, both b_mc), in one launch where
+// both are small.
+size_t prod16_pair_workspace(const Prod &x, const Prod &w);
+hipError_t launch_prod16_pair(int dtype, const Prod &x, const Prod &w, const Workspace &ws,
+                              hipStream_t stream);
+
 // The tile kernel of large products (linear16_big.hip), for operands whose
 // rows take direct 16-byte loads.
 hipError_t launch_prod16_big(int dtype, const Prod &p, hipStream_t stream);
