@@ -468,26 +468,26 @@ def gemm_batched(A, B, C=None, alpha: float = 1.0, beta: float = 0.0, *, trans_a
 # one read of each property): with the helpers above a linear layer took 12 us of
 # host time, with these 9, of which 4 are the library's call and launch.
 
-_torch = None
+_torch = _raw_stream = _get_device = None
 _codes: dict = {}
 
 
 def _import_torch():
-    global _torch
+    global _torch, _raw_stream, _get_device
     import torch
 
     _codes.update({torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16})
+    _raw_stream, _get_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
     _torch = torch
     return torch
 
 
-def _matrix(name, t, rows, cols, dtype, dev):
-    """(address, leading dimension) of a row-major rows x cols matrix."""
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D")
-    r, c = t.shape
-    if r != rows or c != cols:
-        raise ValueError(f"{name} must be ({rows}, {cols}), got ({r}, {c})")
+def _rows(name, t, dtype, dev):
+    """(rows, columns, address, leading dimension) of a row-major matrix."""
+    try:
+        r, c = t.shape
+    except ValueError:
+        raise ValueError(f"{name} must be 2-D") from None
     if t.dtype is not dtype or t.get_device() != dev:
         raise ValueError(f"{name} must be {dtype} on GPU {dev}")
     ld, one = t.stride()
@@ -499,7 +499,15 @@ def _matrix(name, t, rows, cols, dtype, dev):
         ld = c if c > 1 else 1
     if ld > 0x7fffffff or r > 0x7fffffff:
         raise ValueError(f"{name}: sizes and strides must fit 32 bits")
-    return t.data_ptr() or None, ld
+    return r, c, t.data_ptr() or None, ld
+
+
+def _matrix(name, t, rows, cols, dtype, dev):
+    """(address, leading dimension) of a row-major rows x cols matrix."""
+    r, c, p, ld = _rows(name, t, dtype, dev)
+    if r != rows or c != cols:
+        raise ValueError(f"{name} must be ({rows}, {cols}), got ({r}, {c})")
+    return p, ld
 
 
 def _vector(name, t, n, dtype, dev):
@@ -510,31 +518,31 @@ def _vector(name, t, n, dtype, dev):
     return t.data_ptr() or None
 
 
-def _first(name, t, torch):
+def _first(name, t):
     """(dtype code, dtype, device index) that the call's other arrays share."""
     dtype = t.dtype
     code = _codes.get(dtype)
     if code is None:
         raise ValueError(f"{name} must be float32, bfloat16 or float16")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D")
     dev = t.get_device()
-    if dev < 0 or not t.is_cuda:
+    if dev < 0:
+        if t.dim() != 2:
+            raise ValueError(f"{name} must be 2-D")
         raise ValueError(f"{name} must be a GPU tensor")
     return code, dtype, dev
 
 
-def _call(torch, dev, stream, entry, args):
+def _call(dev, stream, entry, args):
     """entry(*args, stream) with the arrays' device current."""
     if stream is None:
-        s = torch._C._cuda_getCurrentRawStream(dev)
+        stream = _raw_stream(dev)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    if _get_device() == dev:
+        st = entry(*args, stream)
     else:
-        s = stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
-    if torch._C._cuda_getDevice() == dev:
-        st = entry(*args, s)
-    else:
-        with torch.cuda.device(dev):
-            st = entry(*args, s)
+        with _torch.cuda.device(dev):
+            st = entry(*args, stream)
     if st != 0:
         raise SgemmError(st)
 
@@ -549,12 +557,12 @@ def linear(X, W, bias=None, *, act: int = ACT_NONE, residual=None, keep_pre: boo
     for linear_backward: (Y, Z).  out and pre receive Y and Z when given (out
     may be residual itself).  Runs asynchronously on ``stream`` (default: the
     current stream of X's device)."""
-    torch = _torch or _import_torch()
-    code, dtype, dev = _first("X", X, torch)
-    M, K = X.shape
-    N = W.shape[0]
-    x, ldx = _matrix("X", X, M, K, dtype, dev)
-    w, ldw = _matrix("W", W, N, K, dtype, dev)
+    _torch or _import_torch()
+    code, dtype, dev = _first("X", X)
+    M, K, x, ldx = _rows("X", X, dtype, dev)
+    N, cols, w, ldw = _rows("W", W, dtype, dev)
+    if cols != K:
+        raise ValueError(f"inner dimensions differ: X is ({M}, {K}), W is ({N}, {cols})")
     b = r = z = None
     ldr = ldz = 0
     if bias is not None:
@@ -571,7 +579,7 @@ def linear(X, W, bias=None, *, act: int = ACT_NONE, residual=None, keep_pre: boo
     elif keep_pre:
         pre = X.new_empty((M, N))
         z, ldz = pre.data_ptr() or None, N or 1
-    _call(torch, dev, stream, _load().sgemm_linear,
+    _call(dev, stream, _load().sgemm_linear,
           (code, M, N, K, x, ldx, w, ldw, b, r, ldr, act, y, ldy, z, ldz))
     return (out, pre) if keep_pre else out
 
@@ -583,14 +591,12 @@ def linear_backward(dY, X, W, Z=None, *, act: int = ACT_NONE, need_x: bool = Tru
     needed.  Z is the activation's input that ``linear(keep_pre=True)`` returned
     (not needed for ACT_NONE); the gradient of a residual is dY itself.  Types,
     layout and stream handling as linear()."""
-    torch = _torch or _import_torch()
-    code, dtype, dev = _first("dY", dY, torch)
-    M, N = dY.shape
-    if X.dim() != 2:
-        raise ValueError("X must be 2-D")
-    K = X.shape[1]
-    g, ldg = _matrix("dY", dY, M, N, dtype, dev)
-    x, ldx = _matrix("X", X, M, K, dtype, dev)
+    _torch or _import_torch()
+    code, dtype, dev = _first("dY", dY)
+    M, N, g, ldg = _rows("dY", dY, dtype, dev)
+    rows, K, x, ldx = _rows("X", X, dtype, dev)
+    if rows != M:
+        raise ValueError(f"dY has {M} rows, X {rows}")
     w, ldw = _matrix("W", W, N, K, dtype, dev)
     z, ldz = None, N or 1
     if act != ACT_NONE:
@@ -608,7 +614,7 @@ def linear_backward(dY, X, W, Z=None, *, act: int = ACT_NONE, need_x: bool = Tru
     if need_bias:
         db = dY.new_empty((N,))
         pb = db.data_ptr() or None
-    _call(torch, dev, stream, _load().sgemm_linear_backward,
+    _call(dev, stream, _load().sgemm_linear_backward,
           (code, M, N, K, g, ldg, z, ldz, act, x, ldx, w, ldw, px, ldk, pw, ldk, pb))
     return dX, dW, db
 
@@ -639,14 +645,13 @@ def moe(X, router, W1, W2, top_k: int, *, act: int = ACT_SILU, renormalize: bool
     T x top_k int32 and float32.  Runs asynchronously on ``stream``
     (default: the current stream of X's device)."""
     torch = _torch or _import_torch()
-    code, dtype, dev = _first("X", X, torch)
+    code, dtype, dev = _first("X", X)
     if W1.dim() != 3 or W2.dim() != 3:
         raise ValueError("W1 and W2 must be 3-D")
-    T, D = X.shape
+    T, D, x, ldx = _rows("X", X, dtype, dev)
     E, _, F = W2.shape
     rows = W1.shape[1]
     gated = int(rows == 2 * F)
-    x, ldx = _matrix("X", X, T, D, dtype, dev)
     wr, ldr = _matrix("router", router, E, D, dtype, dev)
     w1, ld1, step1 = _stack("W1", W1, E, 2 * F if gated else F, D, dtype, dev)
     w2, ld2, step2 = _stack("W2", W2, E, D, F, dtype, dev)
@@ -662,7 +667,7 @@ def moe(X, router, W1, W2, top_k: int, *, act: int = ACT_SILU, renormalize: bool
         ids = X.new_empty((T, top_k), dtype=torch.int32)
         weights = X.new_empty((T, top_k), dtype=torch.float32)
         pi, pw = ids.data_ptr() or None, weights.data_ptr() or None
-    _call(torch, dev, stream, _load().sgemm_moe,
+    _call(dev, stream, _load().sgemm_moe,
           (code, T, D, F, E, top_k, gated, 1 if renormalize else 0, act, x, ldx, wr, ldr, w1, ld1,
            step1, w2, ld2, step2, y, ldy, pi, pw))
     return (out, ids, weights) if return_routing else out
