@@ -411,7 +411,11 @@ Plan16 plan16(const Prod &p) {
     auto tiles = [&](int b) { return (long long)((p.M + b - 1) / b) * ((p.N + b - 1) / b); };
     Plan16 q{};
     q.big = tiles(256) >= kCUs / 2 && a_direct(p, 256) && b_direct(p, 256);
-    q.bm = q.bn = tiles(128) >= kCUs ? 128 : 64;
+    // 128 x 128 where they give more than half the CUs a tile each (6113 x 560 x
+    // 4408, 240 tiles: 53 us, 83 with 64 x 64; 2048 x 1536 x 2048, 192 tiles: 23.3 us
+    // and 24.7; with 144 tiles both take 14.3; with fewer the split costs more:
+    // 2048 x 1024 x 4096, 128 tiles: 36 us and 28)
+    q.bm = q.bn = tiles(128) > kCUs / 2 ? 128 : 64;
     const long long t = tiles(q.bm);
     const int stages = (p.K + kBK - 1) / kBK;
     int s = 1;
