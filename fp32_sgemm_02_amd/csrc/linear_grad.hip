@@ -21,7 +21,6 @@ struct GradArgs {
     const void *dY, *Z;
     void *G, *lo, *db;
     long long lddy, ldz, ldg;
-    int vec;        // 16-byte rows of dY and Z (those of G always are)
     int band;       // rows per band
     int bands;
     float *part;    // bands x N
@@ -43,9 +42,10 @@ __global__ void __launch_bounds__(256) grad_kernel(GradArgs a) {
 #pragma unroll
     for (int e = 0; e < V; ++e) sum[e] = 0.f;
     if (cols > 0) {
-        // (the same for the whole block, so that the loads of several rows run
-        // together)
-        const bool vec = a.vec && (n0 + COLS <= a.N || a.N % V == 0);
+        // 16 bytes at a time (from any address; those of G are aligned) unless N
+        // ends inside a lane's; the same for the whole block, so that the loads of
+        // several rows run together
+        const bool vec = n0 + COLS <= a.N || a.N % V == 0;
 #pragma unroll 2
         for (int r = r0 + rl; r < r1; r += kRowLanes) {
             const T *dy = static_cast<const T *>(a.dY) + (long long)r * a.lddy + n;
@@ -54,9 +54,9 @@ __global__ void __launch_bounds__(256) grad_kernel(GradArgs a) {
             T *lo = a.lo ? static_cast<T *>(a.lo) + (long long)r * a.ldg + n : nullptr;
             T y[V], x[V], o[V], l[V];
             if (vec) {
-                __builtin_memcpy(y, __builtin_assume_aligned(dy, 16), 16);
+                __builtin_memcpy(y, dy, 16);
                 if (ACT != SGEMM_ACT_NONE)
-                    __builtin_memcpy(x, __builtin_assume_aligned(z, 16), 16);
+                    __builtin_memcpy(x, z, 16);
             } else {
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
@@ -189,9 +189,7 @@ hipError_t launch_grad(int dtype, int M, int N, const void *dY, long long lddy, 
                        long long ldz, int act, void *G, void *lo, long long ldg, void *db,
                        float *part, unsigned *count, hipStream_t stream) {
     const Bands b = bands_of(dtype, M, N);
-    const int elem = dtype == kF32 ? 4 : 2;
-    const int vec = rows16(dY, lddy, elem) && (act == SGEMM_ACT_NONE || rows16(Z, ldz, elem));
-    const GradArgs a{M, N, dY, Z, G, lo, db, lddy, ldz, ldg, vec, b.band, b.bands, part, count};
+    const GradArgs a{M, N, dY, Z, G, lo, db, lddy, ldz, ldg, b.band, b.bands, part, count};
     switch (dtype) {
     case SGEMM_DTYPE_BF16: return launch_dt<SGEMM_DTYPE_BF16>(a, act, b.blocks, stream);
     case SGEMM_DTYPE_F16: return launch_dt<SGEMM_DTYPE_F16>(a, act, b.blocks, stream);
