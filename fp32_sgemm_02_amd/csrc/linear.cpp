@@ -126,6 +126,81 @@ int run_linear(int dtype, const Prod &p, hipStream_t stream) {
     });
 }
 
+// An fp32 product of the backward pass with few tiles of C and a long inner
+// length leaves most CUs idle in the plans of single products: its inner
+// length is cut into equal chunks, run as one batch (and one product for what is
+// left over), and the partial products are added in order (7600 x 136 x 589: dX and
+// dW take 29 and 54 us, the two uncut 331; from 128 tiles of 128 x 128 on one
+// product fills the card by itself).
+struct Chunks {
+    int count = 0, k = 0, rest = 0;   // 0: not cut
+    long long ld = 0, step = 0;       // of the partial products
+    size_t bytes = 0, sums = 0;       // the partial products, and the batch's own sums
+};
+
+Problem chunk_of(const Problem &p, const Chunks &c, float *parts) {
+    Problem q = p;
+    q.K = c.k;
+    q.batch = c.count;
+    q.stride_a = p.trans_a ? (long long)c.k * p.lda : c.k;
+    q.stride_b = (long long)c.k * p.ldb;   // (B is never transposed here)
+    q.C = parts;
+    q.ldc = c.ld;
+    q.stride_c = c.step;
+    return q;
+}
+Problem rest_of(const Problem &p, const Chunks &c, float *parts) {
+    Problem q = p;
+    const long long k = (long long)c.k * c.count;
+    q.K = c.rest;
+    q.A = p.trans_a ? p.A + k * p.lda : p.A + k;
+    q.B = p.B + k * p.ldb;
+    q.C = parts + c.count * c.step;
+    q.ldc = c.ld;
+    return q;
+}
+
+Chunks chunks_of(const Problem &p) {
+    Chunks c;
+    if (p.M == 0 || p.N == 0) return c;
+    const long long tiles = (long long)((p.M + 127) / 128) * ((p.N + 127) / 128);
+    // a chunk of 256 at least: enough to pay for writing and adding its result
+    long long n = tiles > 128 ? 1 : 512 / tiles;
+    if (n > p.K / 256) n = p.K / 256;
+    if (n > 32) n = 32;
+    if (n < 2) return c;
+    c.k = (int)(p.K / n / 16 * 16);
+    c.count = p.K / c.k;
+    c.rest = p.K - c.count * c.k;
+    c.ld = (long long)round_up(p.N, 4);
+    c.step = c.ld * p.M;
+    c.bytes = round_up((size_t)c.step * (c.count + 1) * 4, 256);
+    float *at = reinterpret_cast<float *>(uintptr_t{4096});   // (for the plans: an aligned place)
+    c.sums = product_workspace(chunk_of(p, c, at));
+    const size_t r = c.rest ? product_workspace(rest_of(p, c, at)) : 0;
+    if (r > c.sums) c.sums = r;
+    c.sums = round_up(c.sums, 256);
+    return c;
+}
+
+size_t chunked_workspace(const Problem &p) {
+    const Chunks c = chunks_of(p);
+    return c.count ? c.sums + c.bytes : product_workspace(p);
+}
+
+// p with its partial sums (`bytes` as chunked_workspace) at the front of the
+// workspace.
+int run_chunked(const Problem &p, const Workspace &ws, hipStream_t stream) {
+    const Chunks c = chunks_of(p);
+    if (!c.count) return run_in(p, ws, product_workspace(p), stream);
+    float *parts = reinterpret_cast<float *>(static_cast<unsigned char *>(ws.ptr) + c.sums);
+    int st = run_in(chunk_of(p, c, parts), ws, c.sums, stream);
+    if (st == 0 && c.rest) st = run_in(rest_of(p, c, parts), ws, c.sums, stream);
+    if (st != 0) return st;
+    return to_status(launch_sum32(p.M, p.N, parts, c.ld, c.step, c.count + (c.rest ? 1 : 0), p.C,
+                                  p.ldc, stream));
+}
+
 struct Backward {
     int M, N, K;
     const void *dY;
@@ -183,8 +258,8 @@ int run_backward(int dtype, const Backward &b, hipStream_t stream) {
     Problem dw32 = op32(1, b.N, b.K, b.M, g_at, ldg, b.X, b.ldx, b.dW, b.lddw);
     const bool dx_lib = want_dx && !dx_ours, dw_lib = want_dw && !dw_ours;
     size_t scratch = want_db ? grad_workspace(dtype, b.M, b.N) : 0;
-    if (dx_lib && product_workspace(dx32) > scratch) scratch = product_workspace(dx32);
-    if (dw_lib && product_workspace(dw32) > scratch) scratch = product_workspace(dw32);
+    if (dx_lib && chunked_workspace(dx32) > scratch) scratch = chunked_workspace(dx32);
+    if (dw_lib && chunked_workspace(dw32) > scratch) scratch = chunked_workspace(dw32);
     if (dx_ours) {
         const size_t s = ours_workspace(dtype, dx, few);
         if (s > scratch) scratch = s;
@@ -214,12 +289,12 @@ int run_backward(int dtype, const Backward &b, hipStream_t stream) {
         }
         if (pair) return to_status(launch_prod16_pair(dtype, dx, dw, ws, stream));
         if (want_dx) {
-            const int st = dx_lib ? run_in(dx32, ws, scratch, stream)
+            const int st = dx_lib ? run_chunked(dx32, ws, stream)
                                   : to_status(launch_product(dtype, dx, few, ws, stream));
             if (st != 0) return st;
         }
         if (!want_dw) return 0;
-        if (dw_lib) return run_in(dw32, ws, scratch, stream);
+        if (dw_lib) return run_chunked(dw32, ws, stream);
         return to_status(few ? launch_outer(dtype, dw, stream)
                              : launch_product(dtype, dw, false, ws, stream));
     });

@@ -137,6 +137,18 @@ __global__ void __launch_bounds__(256) finish32_kernel(int M, int N, const float
     }
 }
 
+__global__ void __launch_bounds__(256) sum32_kernel(int M, int N, const float *parts, long long ldp,
+                                                    long long step, int count, float *C,
+                                                    long long ldc) {
+    for (int i = blockIdx.y; i < M; i += gridDim.y)
+        for (int j = blockIdx.x * blockDim.x + threadIdx.x; j < N; j += gridDim.x * blockDim.x) {
+            const float *p = parts + (long long)i * ldp + j;
+            float s = 0.f;
+            for (int q = 0; q < count; ++q) s += p[q * step];
+            C[(long long)i * ldc + j] = s;
+        }
+}
+
 struct Bands {
     int blocks, band, bands;
 };
@@ -195,6 +207,14 @@ hipError_t launch_grad(int dtype, int M, int N, const void *dY, long long lddy, 
     case SGEMM_DTYPE_F16: return launch_dt<SGEMM_DTYPE_F16>(a, act, b.blocks, stream);
     default: return launch_dt<kF32>(a, act, b.blocks, stream);
     }
+}
+
+hipError_t launch_sum32(int M, int N, const float *parts, long long ldp, long long step, int count,
+                        float *C, long long ldc, hipStream_t stream) {
+    const int bx = (N + 255) / 256 < 64 ? (N + 255) / 256 : 64, by = M < 65535 ? M : 65535;
+    hipLaunchKernelGGL(sum32_kernel, dim3(bx, by), dim3(256), 0, stream, M, N, parts, ldp, step, count,
+                       C, ldc);
+    return hipGetLastError();
 }
 
 hipError_t launch_finish32(int M, int N, const float *Z, long long ldz, int act, const float *R,

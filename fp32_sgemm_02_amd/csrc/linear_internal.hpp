@@ -97,6 +97,11 @@ struct Moe {
 size_t moe_workspace(const Moe &m);
 hipError_t launch_moe(int dtype, const Moe &m, const Workspace &ws, hipStream_t stream);
 
+// C = the sum of the `count` M x N arrays at `parts`, `step` floats apart with
+// rows of ldp floats, in order.
+hipError_t launch_sum32(int M, int N, const float *parts, long long ldp, long long step, int count,
+                        float *C, long long ldc, hipStream_t stream);
+
 // Y = act(Z) + R elementwise over M x N in fp32, in place where Y is Z.
 hipError_t launch_finish32(int M, int N, const float *Z, long long ldz, int act, const float *R,
                            long long ldr, float *Y, long long ldy, hipStream_t stream);
