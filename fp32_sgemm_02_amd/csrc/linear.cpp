@@ -130,7 +130,7 @@ int run_linear(int dtype, const Prod &p, hipStream_t stream) {
 // length leaves most CUs idle in the plans of single products: its inner
 // length is cut into equal chunks, run as one batch (and one product for what is
 // left over), and the partial products are added in order (7600 x 136 x 589: dX and
-// dW take 29 and 54 us, the two uncut 331; from 128 tiles of 128 x 128 on one
+// dW take 29 and 54 us, the two uncut 331; beyond 128 tiles of 128 x 128 one
 // product fills the card by itself).
 struct Chunks {
     int count = 0, k = 0, rest = 0;   // 0: not cut

@@ -184,6 +184,25 @@ __device__ __forceinline__ uintx4 turned(const uintx4 (&w)[Step<DT>::V], int c) 
     return f;
 }
 
+// v without its first d values (d < V), zeros behind the rest: what a lane does
+// whose columns end inside its 16 bytes, which it loads so that they end with the
+// row (37 x 429 x 921 bf16: dX 20 us and dW 11; value by value 33 and 17).
+template <int DT>
+__device__ __forceinline__ uintx4 without(uintx4 v, int d) {
+    const int dwords = DT == SGEMM_DTYPE_F32 ? d : d >> 1;
+    const bool one = dwords & 1, two = dwords & 2, half = DT != SGEMM_DTYPE_F32 && (d & 1);
+    unsigned u[5];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) u[q] = one ? (q < 3 ? v[q + 1] : 0u) : v[q];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) u[q] = two ? (q < 2 ? u[q + 2] : 0u) : u[q];
+    u[4] = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        v[q] = half ? __builtin_amdgcn_perm(u[q + 1], u[q], 0x05040302u) : u[q];
+    return v;
+}
+
 // dX = G W: a strip of 16 V columns of W per workgroup (V values to 16
 // bytes), k walking W's rows, turned in registers.  LO: G in two parts.
 template <int DT, int TB, bool LO, int NW>
@@ -207,6 +226,11 @@ __global__ void __launch_bounds__(64 * NW) cols_kernel(Prod p, RowsGrid gr) {
     // lanes past the end read the strip's first columns (not stored)
     const bool even = n0 + COLS <= p.N || (p.N % V == 0 && p.N - n0 >= V);
     const T *Bf = static_cast<const T *>(p.B) + (cols >= V ? col : n0);
+    // in a strip that does, the lane's load ends with the row at the latest; only
+    // rows of fewer than V columns are read value by value
+    const bool wide = p.N >= V;
+    const int at_end = even ? 0 : min(col, p.N - V), beyond = even ? 0 : min(col - at_end, V - 1);
+    const T *Be = even ? Bf : static_cast<const T *>(p.B) + at_end;
     auto load = [&](Round &r, int k) {
         const int kg = k + V * g;
         if (even && k + KS <= ke) {
@@ -220,9 +244,29 @@ __global__ void __launch_bounds__(64 * NW) cols_kernel(Prod p, RowsGrid gr) {
             }
             return;
         }
+        if (wide) {
 #pragma unroll
-        for (int e = 0; e < V; ++e)
-            r.w[e] = load_frag<DT>(B + (long long)(kg + e) * p.ldb, kg + e < ke ? cols : 0, Bf);
+            for (int e = 0; e < V; ++e) {
+                const bool in = kg + e < ke;
+                r.w[e] = load_whole<DT>(Be + (long long)(in ? kg + e : ke - 1) * p.ldb, in);
+            }
+            if (!even)
+#pragma unroll
+                for (int e = 0; e < V; ++e) r.w[e] = without<DT>(r.w[e], beyond);
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                r.w[e] = load_frag<DT>(B + (long long)(kg + e) * p.ldb, kg + e < ke ? cols : 0, Bf);
+        }
+        if (k + KS <= ke) {
+#pragma unroll
+            for (int t = 0; t < TB; ++t) {
+                const long long at = (long long)min(16 * t + i, p.M - 1) * p.lda + kg;
+                r.x[t] = load_whole<DT>(static_cast<const T *>(p.A) + at);
+                if constexpr (LO) r.l[t] = load_whole<DT>(static_cast<const T *>(p.lo) + at);
+            }
+            return;
+        }
 #pragma unroll
         for (int t = 0; t < TB; ++t) {
             const long long at = (long long)min(16 * t + i, p.M - 1) * p.lda + kg;
@@ -334,12 +378,17 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(Prod p, int blocks_n) {
     // (X's lanes are dealt so that the four lanes that store one row side by
     // side store 64 bytes in a row)
     const int am = m0 + V * i, bn = n0 + V * (4 * (i & 3) + (i >> 2));
-    // 16-byte loads throughout unless the block ends inside a lane's values;
-    // lanes past an end read the block's first values (not stored), rows past K
-    // the last one (zeroed)
+    // 16-byte loads throughout: where the block ends inside a lane's values they
+    // end with the row and are moved; lanes past an end read values that are not
+    // stored, rows past K the last one (zeroed)
     auto even = [&](int at0, int n) { return at0 + B <= n || (n % V == 0 && n - at0 >= V); };
-    const bool fast = p.K > 0 && even(m0, p.M) && even(n0, p.N);   // K == 0: no row to read
-    const int amf = am + V <= p.M ? am : m0, bnf = bn + V <= p.N ? bn : n0;
+    const bool fast_m = even(m0, p.M), fast_n = even(n0, p.N);
+    // K == 0: no row to read; fewer than V values: value by value
+    const bool fast = p.K > 0 && p.M >= V && p.N >= V;
+    const int amf = fast_m ? (am + V <= p.M ? am : m0) : min(am, p.M - V);
+    const int bnf = fast_n ? (bn + V <= p.N ? bn : n0) : min(bn, p.N - V);
+    const int beyond_m = fast_m ? 0 : min(am - amf, V - 1);
+    const int beyond_n = fast_n ? 0 : min(bn - bnf, V - 1);
     uintx4 fb[S][V];
 #pragma unroll
     for (int s = 0; s < S; ++s) {
@@ -355,6 +404,14 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(Prod p, int blocks_n) {
                 if constexpr (LO)
                     a[1][e] = load_whole<DT>(static_cast<const T *>(p.lo) + kc * p.lda + amf, in);
             }
+            if (!fast_n)
+#pragma unroll
+                for (int e = 0; e < V; ++e) b[e] = without<DT>(b[e], beyond_n);
+            if (!fast_m)
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+#pragma unroll
+                    for (int q = 0; q < PARTS; ++q) a[q][e] = without<DT>(a[q][e], beyond_m);
         } else if (p.K == 0) {   // no row to read: dW is zero
 #pragma unroll
             for (int e = 0; e < V; ++e) {
@@ -451,7 +508,7 @@ PlanRows plan_rows(int dtype, const Prod &p) {
         q.acc = (p.b_mc ? v : 1) * q.tb;   // 16-byte accumulators per lane of a strip
         q.strips = (p.N + q.width - 1) / q.width;
         // split k until two workgroups per CU are in flight, each wave keeping
-        // four steps at least
+        // four steps at least (with one, 64 x 2048 x 512 dX 18 -> 24 us: the join)
         if (q.strips < kCUs && q.strips <= kWorkspaceCounters) {
             s = (2 * kCUs + q.strips - 1) / q.strips;
             const int most = p.K / (kWaves * 4 * step);   // (or two for each of eight waves)

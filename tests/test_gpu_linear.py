@@ -45,6 +45,8 @@ SHAPES = [
     (515, 264, 136), (300, 1111, 640), (1025, 2047, 72), (2048, 2176, 136),
     # 128 tiles of 256 x 256 and more, for each of the three products; one to four stages
     (4100, 2184, 136), (4104, 136, 2184), (200, 4104, 2184), (2568, 3336, 8),
+    # rows that end inside 16 bytes, in each of the three products
+    (37, 429, 921), (2, 536, 76), (20, 45, 133), (64, 7, 131), (5, 131, 7),
     # few tiles of dX or dW and a long inner length
     (3001, 70, 130), (70, 3001, 130), (2048, 128, 64), (90, 1040, 264),
     # products large enough to copy operands whose rows take no 16-byte loads
